@@ -5,7 +5,8 @@ library ``libattn.so`` (built in-tree by ``build.py``); this module checks torch
 tensors, allocates outputs with torch, and passes raw device pointers and the
 current CUDA stream through the C ABI declared in ``include/attn.h``.  There is no
 fallback: if the library is missing or the device is not an sm_100 GPU, calls
-raise.
+raise.  The serving operators (rotary positions, the paged cache, attention of
+drafted tokens over it) are in ``cache.py`` and exported here.
 """
 from __future__ import annotations
 
@@ -16,17 +17,23 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import cache as _cache
+from .cache import KVCache, Rope, rope_append, rope_bwd, rope_fwd, tree_fwd
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libattn.so")
 
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED = 0, 1, 2
 ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT, ATTN_ERR_WORKSPACE = 3, 4, 5
 
-# Every symbol include/attn.h and include/attn_selftest.h declare.
+# Every symbol include/attn.h, include/attn_cache.h and include/attn_selftest.h declare.
 EXPORTED_SYMBOLS = ("attn_fwd", "attn_fwd_ex", "attn_bwd", "attn_bwd_workspace_size",
                     "attn_get_device_status", "attn_status_string", "attn_last_error",
                     "attn_selftest_umma", "attn_fwd_noalloc", "attn_fwd_e4m3",
-                    "attn_selftest_umma_e4m3", "attn_bwd_ex", "attn_selftest_exp2")
+                    "attn_selftest_umma_e4m3", "attn_bwd_ex", "attn_selftest_exp2",
+                    "attn_rope", "attn_rope_append", "attn_cache_alloc", "attn_cache_free",
+                    "attn_cache_fork", "attn_cache_fork_workspace_size", "attn_cache_copy",
+                    "attn_cache_compact", "attn_tree_fwd", "attn_tree_workspace_size")
 
 
 class AttnError(RuntimeError):
@@ -100,6 +107,7 @@ def load_library(path: str = LIB_PATH):
     lib.attn_fwd_noalloc.argtypes = [vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, cf, vp,
                                      ctypes.c_int64, ci, vp]
     lib.attn_fwd_noalloc.restype = ci
+    _cache.declare(lib)
     _lib = lib
     return lib
 
@@ -115,6 +123,9 @@ def last_error() -> str:
 def _check(status: int):
     if status != ATTN_OK:
         raise AttnError(status, last_error())
+
+
+_cache._lib_of, _cache._check = load_library, _check
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:

@@ -1,0 +1,467 @@
+"""Serving operators of libattn: rotary positions, the paged key/value cache, and exact
+attention of new (drafted) tokens over it.
+
+Argument marshalling only, as in the package's other entry points: every step runs in the
+CUDA library through the C ABI of ``include/attn_cache.h``.
+
+One step of speculative decoding, for sequences ``slots`` whose drafted trees are packed by
+``cu_q``::
+
+    cache.alloc(slots, lens_with_drafts)                      # pages for the drafted tokens
+    q = rope_append(cache, q, k, v, cu_q, plan=rope, positions=depths, slots=slots)
+    o, lse = tree_fwd(cache, q, cu_q, mask=tree, slots=slots)
+    cache.compact(cu_q, path, accepted, slots=slots)          # what verification kept
+
+With one token per sequence and no mask this is ordinary decoding.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+_lib_of = None  # set by the package: loads the library
+_check = None   # set by the package: raises AttnError
+
+_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class RopePlan(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("src_batch", ctypes.c_int64), ("src_token", ctypes.c_int64),
+                ("src_head", ctypes.c_int64), ("dst_batch", ctypes.c_int64),
+                ("dst_token", ctypes.c_int64), ("dst_head", ctypes.c_int64)]
+
+
+class CacheView(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("layers", ctypes.c_int),
+                ("pages", ctypes.c_int), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("d", ctypes.c_int), ("slots", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("e4m3", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+_TwoRows = Rows * 2
+
+
+def declare(lib) -> None:
+    """Argument types of the entry points of include/attn_cache.h."""
+    vp, ci, cf, cs = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    for name, args in {
+            "attn_rope": [vp, ci, ci, vp, ci, ci, ci, ci, vp, vp, vp],
+            "attn_rope_append": [vp, ci, vp, vp, vp, vp, ci, ci, vp, vp, vp, vp],
+            "attn_cache_alloc": [vp, vp, vp, ci, vp, vp],
+            "attn_cache_free": [vp, vp, ci, vp],
+            "attn_cache_fork": [vp, vp, vp, ci, vp, vp, cs, vp],
+            "attn_cache_copy": [vp, vp, vp, ci, vp],
+            "attn_cache_compact": [vp, vp, vp, ci, vp, vp, ci, vp],
+            "attn_tree_fwd": [vp, ci, vp, vp, vp, ci, ci, ci, vp, vp, vp, ci, cf, vp, cs, vp],
+    }.items():
+        f = getattr(lib, name)
+        f.argtypes, f.restype = args, ci
+    lib.attn_cache_fork_workspace_size.argtypes = [ci]
+    lib.attn_cache_fork_workspace_size.restype = cs
+    lib.attn_tree_workspace_size.argtypes = [ci]
+    lib.attn_tree_workspace_size.restype = cs
+
+
+def _stream(dev: torch.device, stream: Optional[torch.cuda.Stream], *made) -> int:
+    """The raw stream of a call; tensors this call made are kept until it has run there."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _on(dev: torch.device, f, *args) -> None:
+    """Calls the library with `dev` current; raises on an error status."""
+    if torch._C._cuda_getDevice() == dev.index:
+        st = f(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args)
+    if st:
+        _check(st)
+
+
+def _list(t, name: str, dev: torch.device, n: Optional[int] = None) -> int:
+    """The address of a contiguous int32 list on `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be an int32 tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values")
+    return t.data_ptr()
+
+
+def _cuda(t, name: str):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+class Rope:
+    """Rotary positions of one kind: which values of a head turn, and how fast.
+
+    Pair i of the first ``dim`` values turns by ``position * base**(-2i/dim)``.  The pairs
+    are values (i, i + dim/2), or (2i, 2i+1) with ``interleaved``.  ``scaling`` stretches
+    them for contexts ``factor`` times longer than those of training:
+
+    * ``"linear"``: every frequency divided by ``factor`` (position interpolation);
+    * ``"ntk"``: ``base`` multiplied by ``factor**(dim/(dim-2))``;
+    * ``"yarn"``: frequencies that turn more than ``beta_fast`` times over the
+      ``original_len`` tokens of training stay, those below ``beta_slow`` turns are divided
+      by ``factor``, with a linear ramp over the index between; the rotated values are
+      multiplied by ``1 + 0.1 ln(factor)``.
+
+    ``amplitude`` overrides that multiplier (1 for the other kinds).  The frequencies are
+    kept on ``device`` as exact 64-bit fractions of a turn, so positions may be any int32.
+    """
+
+    def __init__(self, dim: int, base: float = 10000.0, interleaved: bool = False,
+                 scaling: Optional[str] = None, factor: float = 1.0,
+                 original_len: Optional[int] = None, beta_fast: float = 32.0,
+                 beta_slow: float = 1.0, amplitude: Optional[float] = None, device="cuda"):
+        if dim <= 0 or dim % 16:
+            raise ValueError("dim must be a positive multiple of 16")
+        if not (math.isfinite(base) and base > 1.0):
+            raise ValueError("base must be finite and > 1")
+        if not (math.isfinite(factor) and factor >= 1.0):
+            raise ValueError("factor must be finite and >= 1")
+        if scaling not in (None, "linear", "ntk", "yarn"):
+            raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+        self.dim, self.interleaved = dim, bool(interleaved)
+        amp = 1.0
+        if scaling == "ntk":
+            base = base * factor ** (dim / (dim - 2))
+        freqs = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+        if scaling == "linear":
+            freqs = [f / factor for f in freqs]
+        if scaling == "yarn":
+            if original_len is None or original_len <= 0 or not beta_fast > beta_slow > 0:
+                raise ValueError("yarn needs original_len > 0 and beta_fast > beta_slow > 0")
+
+            def index(turns):
+                return dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+            lo = max(math.floor(index(beta_fast)), 0)
+            hi = min(math.ceil(index(beta_slow)), dim // 2 - 1)
+            for i, f in enumerate(freqs):
+                ramp = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+                freqs[i] = f * (1 - ramp) + f / factor * ramp
+            amp = 0.1 * math.log(factor) + 1.0
+        self.amplitude = amp if amplitude is None else float(amplitude)
+        if not (math.isfinite(self.amplitude) and self.amplitude > 0):
+            raise ValueError("amplitude must be finite and > 0")
+        # f < 1, so a fraction of a turn is below 2^62 and fits int64
+        self.turns = torch.tensor([round(f / (2 * math.pi) * 2.0 ** 64) for f in freqs],
+                                  dtype=torch.int64).to(device)
+        self._view = RopePlan(self.turns.data_ptr(), dim, int(self.interleaved), self.amplitude)
+
+
+def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
+    lib = _lib_of()
+    _cuda(q, "q")
+    dev, dtype = q.device, q.dtype
+    if dtype not in _TYPES:
+        raise ValueError("q must be bfloat16, float16 or float32")
+    if plan.turns.device != dev:
+        raise ValueError(f"the plan must be on {dev}")
+    packed = cu_seqlens is not None
+    lead = q.shape[:-2]
+    if q.dim() != (3 if packed else 4):
+        raise ValueError("packed q must be [T, H, d]" if packed else "dense q must be [B, N, H, d]")
+    if out is None:
+        out = (torch.empty(q.shape, dtype=dtype, device=dev),
+               None if k is None else torch.empty(k.shape, dtype=dtype, device=dev))
+        made = out
+    else:
+        made = ()
+        if k is None and isinstance(out, torch.Tensor):
+            out = (out, None)
+    rows = _TwoRows()
+    for i, (x, y, name) in enumerate(((q, out[0], "q"), (k, out[1], "k"))):
+        if x is None:
+            continue
+        _cuda(x, name)
+        _cuda(y, f"out of {name}")
+        if x.dtype != dtype or y.dtype != dtype or x.device != dev or y.device != dev:
+            raise ValueError("q, k and out must share a type and a device")
+        if x.shape[:-2] != lead or x.dim() != q.dim() or x.shape[-1] != q.shape[-1]:
+            raise ValueError("q and k must hold the same tokens and head dim")
+        if y.shape != x.shape:
+            raise ValueError(f"out of {name} has the wrong shape")
+        sx, sy = x.stride(), y.stride()
+        if x.numel() and (sx[-1] != 1 or sy[-1] != 1):
+            raise ValueError(f"the values of a head of {name} must be contiguous")
+        r = rows[i]
+        r.src, r.dst, r.heads = x.data_ptr(), y.data_ptr(), x.shape[-2]
+        r.src_token, r.src_head, r.dst_token, r.dst_head = sx[-3], sx[-2], sy[-3], sy[-2]
+        if not packed:
+            r.src_batch, r.dst_batch = sx[0], sy[0]
+    B, N = (cu_seqlens.numel() - 1, lead[0]) if packed else lead
+    tokens = lead[0] if packed else B * N
+    pos = None if positions is None else _list(positions, "positions", dev, tokens)
+    cu = None if cu_seqlens is None else _list(cu_seqlens, "cu_seqlens", dev)
+    _on(dev, lib.attn_rope, ctypes.byref(plan._view), inverse, _TYPES[dtype], rows,
+        1 if k is None else 2, q.shape[-1], B, N, cu, pos, _stream(dev, stream, *made))
+    return out[0] if k is None else (out[0], out[1])
+
+
+def rope_fwd(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None,
+             positions: Optional[torch.Tensor] = None,
+             cu_seqlens: Optional[torch.Tensor] = None, out=None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Rotates q, and k with it, by their tokens' positions, in one launch.
+
+    Dense ``[B, N, H, d]`` or, with ``cu_seqlens`` (int32 ``[B+1]``), packed ``[T, H, d]``;
+    bf16, fp16 or fp32.  Token and head strides may be anything that keeps rows 16-byte
+    aligned (slices of a joint projection); the head counts of q and k may differ.
+    ``positions`` is int32, one per token (default: its index in its sequence; packed rows
+    that belong to no sequence are then left unwritten).  ``out=(q_out, k_out)`` receives the
+    results; the inputs themselves are allowed (in place).  Returns (q', k'), or q' alone
+    without k."""
+    return _rope(plan, 0, q, k, positions, cu_seqlens, out, stream)
+
+
+def rope_bwd(plan: Rope, dq: torch.Tensor, dk: Optional[torch.Tensor] = None,
+             positions: Optional[torch.Tensor] = None,
+             cu_seqlens: Optional[torch.Tensor] = None, out=None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """The gradients of ``rope_fwd`` with respect to its q and k, from those of its results:
+    the rotation by the negative angles.  Arguments as there."""
+    return _rope(plan, 1, dq, dk, positions, cu_seqlens, out, stream)
+
+
+class KVCache:
+    """A paged key/value cache on one GPU.
+
+    ``k``, ``v``: ``[layers, pages, page_size, heads, d]`` (a 4-D tensor is one layer), bf16, or
+    float8_e4m3fn holding the real values divided by ``k_scale`` / ``v_scale``.
+    ``page_table``: int32 ``[slots, max_pages]``; ``lens``: int32 ``[slots]``, the tokens of each
+    slot; ``refs``: int32 ``[pages]``, how many slots hold a page (0: free).  All contiguous, on
+    one device; the cache works on these tensors and keeps nothing else.  Page sizes are
+    powers of two from 16 to 1024, d is 64 or 128.
+
+    The methods change the state on the device and synchronise nothing.  What only the
+    device sees (a bad slot or page number, an inconsistent length) leaves that
+    sequence alone and is reported by ``get_device_status``.  Calls that change
+    one cache must be ordered, e.g. issued on one stream."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor,
+                 lens: torch.Tensor, refs: torch.Tensor, k_scale: float = 1.0,
+                 v_scale: float = 1.0):
+        for t, name in ((k, "k"), (v, "v")):
+            _cuda(t, name)
+            if t.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+                raise ValueError(f"{name} must be bfloat16 or float8_e4m3fn")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+        if k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("k and v must share shape, type and device")
+        if k.dim() not in (4, 5):
+            raise ValueError("k must be [layers, pages, page_size, heads, d]")
+        layers, pages, page_size, heads, d = (1, *k.shape) if k.dim() == 4 else k.shape
+        dev = k.device
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be [slots, max_pages]")
+        slots, max_pages = page_table.shape
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        if not e4m3 and (k_scale != 1.0 or v_scale != 1.0):
+            raise ValueError("scales belong to an E4M3 cache")
+        self._k, self._v, self._table, self._lens, self._refs = k, v, page_table, lens, refs
+        self.device, self.dtype, self.d, self.heads = dev, k.dtype, d, heads
+        self.layers, self.pages, self.page_size = layers, pages, page_size
+        self.slots, self.max_pages = slots, max_pages
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self._view = CacheView(k.data_ptr(), v.data_ptr(), _list(page_table, "page_table", dev),
+                               _list(lens, "lens", dev, slots), _list(refs, "refs", dev, pages),
+                               layers, pages, page_size, heads, d, slots, max_pages, int(e4m3),
+                               self.k_scale, self.v_scale)
+        self._ref = ctypes.byref(self._view)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, page_size: int, heads: int, d: int, slots: int,
+              max_pages: int, dtype=torch.bfloat16, device="cuda", k_scale: float = 1.0,
+              v_scale: float = 1.0) -> "KVCache":
+        """A cache with every page free and every slot empty."""
+        shape = (layers, pages, page_size, heads, d)
+        i32 = dict(dtype=torch.int32, device=device)
+        return cls(torch.empty(shape, dtype=dtype, device=device),
+                   torch.empty(shape, dtype=dtype, device=device),
+                   torch.full((slots, max_pages), -1, **i32), torch.zeros(slots, **i32),
+                   torch.zeros(pages, **i32), k_scale, v_scale)
+
+    # The tensors are fixed for the cache's life: the library is given their addresses.
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    page_table = property(lambda self: self._table)
+    lens = property(lambda self: self._lens)
+    refs = property(lambda self: self._refs)
+
+    def alloc(self, slots: torch.Tensor, new_lens: torch.Tensor,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Grows slot ``slots[i]`` to ``new_lens[i]`` tokens.  Pages are handed out in order
+        of i, lowest number first; returns int32 ``granted[i]``: 1 iff request i needs no page
+        or requests 0..i need no more than are free.  One not granted changes nothing."""
+        lib, dev, n = _lib_of(), self.device, slots.numel()
+        granted = torch.empty(n, dtype=torch.int32, device=dev)
+        _on(dev, lib.attn_cache_alloc, self._ref, _list(slots, "slots", dev),
+            _list(new_lens, "new_lens", dev, n), n, granted.data_ptr(),
+            _stream(dev, stream, granted))
+        return granted
+
+    def free(self, slots: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Empties the slots; pages that no other slot holds become free."""
+        dev = self.device
+        _on(dev, _lib_of().attn_cache_free, self._ref, _list(slots, "slots", dev), slots.numel(),
+            _stream(dev, stream))
+
+    def fork(self, src: torch.Tensor, dst: torch.Tensor,
+             stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+        """Forks slot ``src[i]`` into the empty slot ``dst[i]``: full pages are shared, the
+        tokens of a last page that is not full are copied to a new one, in every layer.
+        Returns ``granted`` as ``alloc`` does."""
+        lib, dev, n = _lib_of(), self.device, src.numel()
+        granted = torch.empty(n, dtype=torch.int32, device=dev)
+        ws = torch.empty(max(lib.attn_cache_fork_workspace_size(n), 16), dtype=torch.uint8,
+                         device=dev)
+        _on(dev, lib.attn_cache_fork, self._ref, _list(src, "src", dev),
+            _list(dst, "dst", dev, n), n, granted.data_ptr(), ws.data_ptr(), ws.numel(),
+            _stream(dev, stream, granted, ws))
+        return granted
+
+    def copy(self, src: torch.Tensor, dst: torch.Tensor,
+             stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Copies page ``src[i]`` to page ``dst[i]`` in every layer (the tables stay as they
+        are).  Of a destination named twice the last copy counts; a source that is also a
+        destination is refused."""
+        dev, n = self.device, src.numel()
+        _on(dev, _lib_of().attn_cache_copy, self._ref, _list(src, "src", dev),
+            _list(dst, "dst", dev, n), n, _stream(dev, stream))
+
+    def compact(self, cu_q: torch.Tensor, path: torch.Tensor, accepted: torch.Tensor,
+                slots: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Keeps the accepted path of each sequence's drafted tokens (its last ``cu_q[b+1] -
+        cu_q[b]`` tokens): ``path[b, :accepted[b]]``, strictly increasing, names which of them
+        stay; they move together behind the context in every layer, and surplus pages are
+        released.  ``path`` is int32 ``[B, width]``; ``slots`` defaults to 0..B-1."""
+        dev, B = self.device, cu_q.numel() - 1
+        if path.dim() != 2 or path.shape[0] != B:
+            raise ValueError("path must be [B, width]")
+        _on(dev, _lib_of().attn_cache_compact, self._ref, _list(cu_q, "cu_q", dev),
+            _list(path, "path", dev), path.shape[1], _list(accepted, "accepted", dev, B),
+            None if slots is None else _list(slots, "slots", dev, B), B, _stream(dev, stream))
+
+
+def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor,
+                cu_q: torch.Tensor, plan: Optional[Rope] = None,
+                positions: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+                layer: int = 0, out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Writes new tokens into a layer of the cache and rotates their queries, in one launch.
+
+    q ``[T, Hq, d]`` and k, v ``[T, heads, d]`` (bf16; strides as in ``rope_fwd``) are packed by
+    ``cu_q`` (int32 ``[B+1]``); sequence b is slot ``slots[b]`` (default b), and its tokens are the
+    last ones of that slot: ``alloc`` first.  q and k turn by ``plan`` (None: not at all) at
+    ``positions`` (int32 ``[T]``; default: the token's place in the cache).  Returns the rotated q
+    (``out``; q itself is allowed), or None without q."""
+    lib = _lib_of()
+    dev = cache.device
+    rows = []
+    if q is not None and out is None:
+        _cuda(q, "q")
+        out, made = torch.empty(q.shape, dtype=q.dtype, device=dev), True
+    else:
+        made = False
+    for x, y, name in ((q, out, "q"), (k, None, "k"), (v, None, "v")):
+        if x is None:
+            rows.append(None)
+            continue
+        _cuda(x, name)
+        if x.dtype != torch.bfloat16 or x.device != dev:
+            raise ValueError(f"{name} must be bfloat16 on {dev}")
+        if x.dim() != 3 or x.shape[0] != k.shape[0] or x.shape[2] != cache.d:
+            raise ValueError(f"{name} must be [T, H, {cache.d}]")
+        sx = x.stride()
+        if x.numel() and sx[2] != 1:
+            raise ValueError(f"the values of a head of {name} must be contiguous")
+        r = Rows(x.data_ptr(), None, x.shape[1], 0, sx[0], sx[1], 0, 0, 0)
+        if y is not None:
+            _cuda(y, "out")
+            if y.shape != x.shape or y.dtype != x.dtype or y.device != dev or (y.numel() and y.stride(2) != 1):
+                raise ValueError("out must be like q")
+            r.dst, r.dst_token, r.dst_head = y.data_ptr(), y.stride(0), y.stride(1)
+        rows.append(ctypes.byref(r))
+    if plan is not None and plan.turns.device != dev:
+        raise ValueError(f"the plan must be on {dev}")
+    T, B = k.shape[0], cu_q.numel() - 1
+    _on(dev, lib.attn_rope_append, cache._ref, layer,
+        None if plan is None else ctypes.byref(plan._view), rows[0], rows[1], rows[2], B, T,
+        _list(cu_q, "cu_q", dev), None if slots is None else _list(slots, "slots", dev, B),
+        None if positions is None else _list(positions, "positions", dev, T),
+        _stream(dev, stream, out if made else None))
+    return out if q is not None else None
+
+
+def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
+             mask: Optional[torch.Tensor] = None, slots: Optional[torch.Tensor] = None,
+             layer: int = 0, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+             lse: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Exact attention of each sequence's newest tokens over its slot of the cache.
+
+    q ``[T, Hq, d]`` (bf16, contiguous, rotated) is packed by ``cu_q`` (int32 ``[B+1]``); the
+    tokens of sequence b are the last ones of slot ``slots[b]`` (default b), already in the cache.
+    Query heads share the cache's heads in groups of ``Hq / heads``.  Every token sees the
+    context before them; among them, token t sees token j iff ``mask[t, j]`` (bool or uint8
+    ``[T, width]``, j within the sequence, at most 256 drafted tokens each), or iff j <= t
+    without a mask.  Returns (O ``[T, Hq, d]`` bf16, LSE ``[Hq, T]`` fp32, natural log); a token
+    that sees nothing gets 0 and -inf.  The workspace is allocated with torch."""
+    lib = _lib_of()
+    dev = cache.device
+    _cuda(q, "q")
+    if q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+        raise ValueError(f"q must be a contiguous bfloat16 tensor on {dev}")
+    if q.dim() != 3 or q.shape[2] != cache.d:
+        raise ValueError(f"q must be [T, Hq, {cache.d}]")
+    T, Hq, d = q.shape
+    B = cu_q.numel() - 1
+    made_o, made_l = out is None, lse is None
+    if made_o:
+        out = torch.empty_like(q)
+    elif not (out.is_cuda and out.device == dev and out.dtype == torch.bfloat16
+              and out.shape == q.shape and out.is_contiguous()):
+        raise ValueError("out must be like q")
+    if made_l:
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    elif not (lse.is_cuda and lse.device == dev and lse.dtype == torch.float32
+              and tuple(lse.shape) == (Hq, T) and lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 [Hq, T]")
+    m, width = None, 0
+    if mask is not None:
+        _cuda(mask, "mask")
+        if mask.dtype not in (torch.bool, torch.uint8) or mask.device != dev:
+            raise ValueError(f"mask must be bool or uint8 on {dev}")
+        if mask.dim() != 2 or mask.shape[0] != T or not mask.is_contiguous():
+            raise ValueError("mask must be a contiguous [T, width]")
+        m, width = mask.data_ptr(), mask.shape[1]
+    bytes_ = lib.attn_tree_workspace_size(d)
+    ws = torch.empty(max(bytes_, 256), dtype=torch.uint8, device=dev)
+    _on(dev, lib.attn_tree_fwd, cache._ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
+        Hq, B, T, _list(cu_q, "cu_q", dev),
+        None if slots is None else _list(slots, "slots", dev, B), m, width,
+        1.0 / math.sqrt(d) if scale is None else float(scale), ws.data_ptr(), ws.numel(),
+        _stream(dev, stream, ws, out if made_o else None, lse if made_l else None))
+    return out, lse

@@ -204,6 +204,15 @@ attn_status_t prepare_selftest(int** err, bool (**mk)(CUtensorMap*, const void*,
   return ATTN_OK;
 }
 
+attn_status_t prepare_device(int** err, int* sms) {
+  DeviceState* dev = nullptr;
+  const attn_status_t st = device_state(&dev);
+  if (st != ATTN_OK) return st;
+  *err = dev->err;
+  *sms = dev->sms;
+  return ATTN_OK;
+}
+
 attn_status_t load_tensor_map_encoder() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_encode) return ATTN_OK;

@@ -51,6 +51,9 @@ attn_status_t launch_planned_fwd(const FwdCall& c, const FwdPlan& pl, const attn
                                  attn_stream_t stream);
 // Looks up the driver's tensor-map encoder once per process.
 attn_status_t load_tensor_map_encoder();
+// Prepares the current device (as every entry point does on its first call) and gives
+// its error word and SM count.
+attn_status_t prepare_device(int** err, int* sms);
 // Records `message` as the calling thread's last error and returns `s`.
 attn_status_t report(attn_status_t s, const char* message);
 

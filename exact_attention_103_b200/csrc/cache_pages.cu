@@ -1,0 +1,428 @@
+// cache_pages.cu -- the pages of the key/value cache: handing out, sharing, copying,
+// moving together and releasing them (include/attn_cache.h).
+//
+// The state is a table of page numbers per slot, a length per slot and a reference
+// count per page.  Free pages are those with count 0, handed out lowest number first in
+// the order of the requests, so results never depend on timing.  All of it is
+// integer bookkeeping of a few kilobytes, bound by latency; the copies are bound by HBM.
+#include <climits>
+#include <cuda_runtime.h>
+
+#include "cache_ops.h"
+
+namespace attn {
+namespace {
+
+constexpr int kBlock = 1024;     // the one block that hands out pages
+constexpr int kPagesPerThread = 16;
+
+__device__ __forceinline__ int pages_of(int tokens, int page_size) {
+  return static_cast<int>((static_cast<int64_t>(tokens) + page_size - 1) / page_size);
+}
+
+// Exclusive prefix sum of one value per thread of the block, and the block's total.
+__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += n;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  const int before = warp ? warp_sums[warp - 1] : 0;
+  total = warp_sums[31];
+  __syncthreads();
+  return before + incl - v;
+}
+
+// One fork, decided by the first kernel and carried out by the second.
+struct ForkItem {
+  int src, dst, len;  // len 0: nothing to do
+  int fresh;          // page of the copied tail (len % page_size != 0)
+};
+
+// Grants requests for pages.  alloc: slot a[i] grows to b[i] tokens.  FORK: slot a[i]
+// is forked into slot b[i] (the pages of its full part and the copies follow in
+// fork_kernel).  Shared memory: owner[slots] (first request that names a slot),
+// upto[n] (pages needed by requests 0..i).
+template <bool FORK>
+__global__ void __launch_bounds__(kBlock) grant_kernel(const attn_cache_t c, const int32_t* a, const int32_t* b, int n,
+                                                       int32_t* granted, ForkItem* items, int* err) {
+  extern __shared__ int shared[];
+  __shared__ int warp_sums[32];
+  int* owner = shared;
+  int* upto = shared + c.slots;
+  const int tid = threadIdx.x;
+  const int32_t* target = FORK ? b : a;  // the slot that is written
+  for (int s = tid; s < c.slots; s += kBlock) owner[s] = INT_MAX;
+  __syncthreads();
+  for (int i = tid; i < n; i += kBlock) {
+    const int s = __ldg(target + i);
+    if (s >= 0 && s < c.slots) atomicMin(&owner[s], i);
+  }
+  __syncthreads();
+  // Each thread takes consecutive requests, so that the prefix sum follows their order.
+  const int per = (n + kBlock - 1) / kBlock;
+  const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int s = __ldg(target + i);
+    bool ok = s >= 0 && s < c.slots && owner[s] == i;
+    int site = kSiteSlot, need = 0;
+    if (FORK) {
+      const int from = __ldg(a + i);
+      ok = ok && from >= 0 && from < c.slots && from != s;
+      if (ok) {
+        const int len = c.lens[from];
+        site = kSiteLength;
+        ok = c.lens[s] == 0 && len >= 0 && len <= static_cast<int64_t>(c.max_pages) * c.page_size;
+        if (ok) need = (len & (c.page_size - 1)) ? 1 : 0;
+      }
+    } else if (ok) {
+      const int len = c.lens[s], want = __ldg(b + i);
+      site = kSiteLength;
+      ok = len >= 0 && want >= len && want <= static_cast<int64_t>(c.max_pages) * c.page_size;
+      if (ok) need = pages_of(want, c.page_size) - pages_of(len, c.page_size);
+    }
+    if (!ok) record_invalid(err, site);
+    granted[i] = ok;
+    sum += need;
+    upto[i] = sum;  // within the thread; the threads before are added below
+  }
+  int total;
+  const int before = block_scan(sum, warp_sums, total);
+  for (int i = i0; i < i1; ++i) upto[i] += before;
+  __syncthreads();
+  // The free pages, lowest first: each thread counts its pages of a stretch, a
+  // prefix sum ranks them, and page number `rank` goes to the request it falls into.
+  int found = 0;
+  for (int base = 0; base < c.pages && found < total; base += kBlock * kPagesPerThread) {
+    const int p0 = base + tid * kPagesPerThread;
+    unsigned free_bits = 0;
+    if (p0 + kPagesPerThread <= c.pages && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
+#pragma unroll
+      for (int k = 0; k < kPagesPerThread / 4; ++k) {
+        const int4 w = reinterpret_cast<const int4*>(c.refs + p0)[k];
+        free_bits |= ((w.x == 0) | ((w.y == 0) << 1) | ((w.z == 0) << 2) | ((w.w == 0) << 3)) << (4 * k);
+      }
+    } else {
+      for (int k = 0; k < kPagesPerThread; ++k)
+        if (p0 + k < c.pages && c.refs[p0 + k] == 0) free_bits |= 1u << k;
+    }
+    int here;
+    int rank = found + block_scan(__popc(free_bits), warp_sums, here);
+    for (; free_bits && rank < total; ++rank, free_bits &= free_bits - 1) {
+      const int page = p0 + __ffs(free_bits) - 1;
+      int lo = 0, hi = n - 1;  // the first request with upto > rank
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (upto[mid] > rank) hi = mid; else lo = mid + 1;
+      }
+      c.refs[page] = 1;
+      if (FORK) {
+        items[lo].fresh = page;
+      } else {
+        const int s = __ldg(a + lo);
+        const int k = pages_of(c.lens[s], c.page_size) + rank - (lo ? upto[lo - 1] : 0);
+        c.page_table[static_cast<int64_t>(s) * c.max_pages + k] = page;
+      }
+    }
+    found += here;
+  }
+  __syncthreads();
+  for (int i = i0; i < i1; ++i) {
+    const int first = i ? upto[i - 1] : 0, need = upto[i] - first;
+    bool ok = granted[i] != 0;
+    const int s = __ldg(target + i);
+    if (ok && need > 0 && upto[i] > found) {
+      ok = false;
+      // What it did get goes back (a fork needs one page: it got none).
+      for (int k = 0; !FORK && k < found - first; ++k) {
+        int32_t* e = c.page_table + static_cast<int64_t>(s) * c.max_pages + pages_of(c.lens[s], c.page_size) + k;
+        c.refs[*e] = 0;
+        *e = -1;
+      }
+    }
+    granted[i] = ok;
+    if (FORK) {
+      items[i].src = __ldg(a + i);
+      items[i].dst = s;
+      items[i].len = ok ? c.lens[items[i].src] : 0;
+    }
+  }
+  __syncthreads();  // every length has been read
+  for (int i = i0; i < i1; ++i) {
+    if (!granted[i]) continue;
+    const int s = __ldg(target + i);
+    c.lens[s] = FORK ? items[i].len : __ldg(b + i);
+  }
+}
+
+// Copies `bytes` (a multiple of 16) by the block, 16 bytes per thread and step.
+__device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int64_t bytes) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int64_t n = bytes / 16;
+  int64_t i = threadIdx.x;
+  for (; i + 3 * blockDim.x < n; i += 4 * blockDim.x) {
+    uint4 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = s[i + k * blockDim.x];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) d[i + k * blockDim.x] = w[k];
+  }
+  for (; i < n; i += blockDim.x) d[i] = s[i];
+}
+
+__device__ __forceinline__ int64_t row_bytes(const attn_cache_t& c) {
+  return static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2);
+}
+// K (kv = 0) or V of layer l, row `row` of its pages.
+__device__ __forceinline__ uint8_t* cache_row(const attn_cache_t& c, int l, int kv, int64_t row) {
+  return static_cast<uint8_t*>(kv ? c.v : c.k) +
+         (static_cast<int64_t>(l) * c.pages * c.page_size + row) * row_bytes(c);
+}
+
+// Block (i, 0) writes the table row and references of fork i; block (i, 1 + y) copies
+// the tail's tokens of one layer's K or V.
+__global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* err) {
+  const ForkItem it = items[blockIdx.x];
+  if (it.len <= 0) return;
+  const int full = it.len / c.page_size, part = it.len & (c.page_size - 1);
+  const int32_t* from = c.page_table + static_cast<int64_t>(it.src) * c.max_pages;
+  if (blockIdx.y == 0) {
+    int32_t* to = c.page_table + static_cast<int64_t>(it.dst) * c.max_pages;
+    for (int m = threadIdx.x; m < full; m += blockDim.x) {
+      const int p = from[m];
+      if (p < 0 || p >= c.pages) record_invalid(err, kSitePage);
+      else atomicAdd(c.refs + p, 1);
+      to[m] = p;
+    }
+    if (part && threadIdx.x == 0) to[full] = it.fresh;
+    return;
+  }
+  if (!part) return;
+  const int old = from[full];
+  if (old < 0 || old >= c.pages) {
+    if (threadIdx.x == 0) record_invalid(err, kSitePage);
+    return;
+  }
+  const int y = blockIdx.y - 1;
+  copy_bytes(cache_row(c, y >> 1, y & 1, static_cast<int64_t>(old) * c.page_size),
+             cache_row(c, y >> 1, y & 1, static_cast<int64_t>(it.fresh) * c.page_size), part * row_bytes(c));
+}
+
+// Takes a reference from entries [m0, m1) of a slot's table row and clears them.
+__device__ __forceinline__ void release(const attn_cache_t& c, int slot, int m0, int m1, int* err) {
+  int32_t* row = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
+  for (int m = m0 + threadIdx.x; m < m1; m += blockDim.x) {
+    const int p = row[m];
+    row[m] = -1;
+    if (p < 0 || p >= c.pages) {
+      record_invalid(err, kSitePage);
+    } else if (atomicSub(c.refs + p, 1) <= 0) {
+      atomicAdd(c.refs + p, 1);
+      record_invalid(err, kSitePage);
+    }
+  }
+}
+
+__global__ void free_kernel(const attn_cache_t c, const int32_t* slots, int* err) {
+  __shared__ int len;
+  const int slot = __ldg(slots + blockIdx.x);
+  if (slot < 0 || slot >= c.slots) {
+    if (threadIdx.x == 0) record_invalid(err, kSiteSlot);
+    return;
+  }
+  if (threadIdx.x == 0) len = atomicExch(c.lens + slot, 0);  // named twice: the second finds 0
+  __syncthreads();
+  if (len <= 0) return;
+  release(c, slot, 0, min(pages_of(len, c.page_size), c.max_pages), err);
+}
+
+__global__ void copy_kernel(const attn_cache_t c, const int32_t* src, const int32_t* dst, int n, int chunks, int* err) {
+  const int i = blockIdx.x;
+  const int from = __ldg(src + i), to = __ldg(dst + i);
+  if (from < 0 || from >= c.pages || to < 0 || to >= c.pages) {
+    if (threadIdx.x == 0) record_invalid(err, kSitePage);
+    return;
+  }
+  if (from == to) return;
+  bool later = false, written = false;
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int o = __ldg(dst + j);
+    const bool moves = __ldg(src + j) != o;  // a page copied onto itself is not written
+    later |= moves && j > i && o == to;
+    written |= moves && o == from;
+  }
+  later = __syncthreads_or(later);
+  written = __syncthreads_or(written);
+  if (written && threadIdx.x == 0) record_invalid(err, kSiteCopyOverlap);
+  if (later || written) return;
+  const int64_t bytes = row_bytes(c) * c.page_size, part = bytes / chunks;
+  for (int y = blockIdx.y; y < c.layers * 2 * chunks; y += gridDim.y) {
+    const int lk = y / chunks, ch = y - lk * chunks;
+    copy_bytes(cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(from) * c.page_size) + ch * part,
+               cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(to) * c.page_size) + ch * part, part);
+  }
+}
+
+// What compact does with sequence b; decided the same way by both of its kernels.
+struct Kept {
+  int slot, base, len, count;
+  bool ok;
+};
+__device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
+                                        const int32_t* accepted, const int32_t* slots, int b, int* err) {
+  Kept k;
+  k.slot = slots ? __ldg(slots + b) : b;
+  int bad = 0;
+  if (k.slot < 0 || k.slot >= c.slots) {
+    bad = kSiteSlot;
+    k.len = k.base = k.count = 0;
+  } else {
+    const int n = __ldg(cu_q + b + 1) - __ldg(cu_q + b);
+    k.len = c.lens[k.slot];
+    k.count = __ldg(accepted + b);
+    k.base = k.len - n;
+    if (n < 0 || k.base < 0 || k.len > static_cast<int64_t>(c.max_pages) * c.page_size) bad = kSiteLength;
+    else if (k.count < 0 || k.count > n || k.count > width) bad = kSitePath;
+    if (!bad) {
+      const int32_t* row = path + static_cast<int64_t>(b) * width;
+      for (int i = threadIdx.x; i < k.count; i += blockDim.x) {
+        const int p = __ldg(row + i);
+        if (p >= n || p <= (i ? __ldg(row + i - 1) : -1)) bad = kSitePath;
+      }
+    }
+    for (int j = threadIdx.x; slots && j < b; j += blockDim.x)
+      if (__ldg(slots + j) == k.slot) bad = kSiteSlot;
+  }
+  if (bad) record_invalid(err, bad);
+  k.ok = !__syncthreads_or(bad);
+  return k;
+}
+
+constexpr int kMoves = 128;  // moves whose rows are looked up together
+
+// Block (b, layer and K/V, columns): moves the accepted tokens' rows.  A thread owns 16
+// bytes of the row and takes the moves in order.  Move i reads position path[i] >= i and
+// writes position i, so no later move reads what an earlier one wrote: the reads of 8
+// moves may go before their writes.
+__global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
+                               const int32_t* accepted, const int32_t* slots, int* err) {
+  __shared__ int64_t from[kMoves], to[kMoves];
+  const int b = blockIdx.x;
+  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, b, err);
+  if (!k.ok) return;
+  const int l = blockIdx.y >> 1, kv = blockIdx.y & 1;
+  const int64_t rb = row_bytes(c);
+  const int64_t col = (static_cast<int64_t>(blockIdx.z) * blockDim.x + threadIdx.x) * 16;
+  uint8_t* base = cache_row(c, l, kv, 0) + col;
+  const int32_t* row = c.page_table + static_cast<int64_t>(k.slot) * c.max_pages;
+  for (int m0 = 0; m0 < k.count; m0 += kMoves) {
+    const int m = min(kMoves, k.count - m0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += blockDim.x) {
+      const int x = k.base + __ldg(path + static_cast<int64_t>(b) * width + m0 + i), y = k.base + m0 + i;
+      const int px = row[x / c.page_size], py = row[y / c.page_size];
+      const bool ok = px >= 0 && px < c.pages && py >= 0 && py < c.pages;
+      if (!ok) record_invalid(err, kSitePage);
+      from[i] = (ok && x != y) ? static_cast<int64_t>(px) * c.page_size + (x & (c.page_size - 1)) : -1;
+      to[i] = static_cast<int64_t>(py) * c.page_size + (y & (c.page_size - 1));
+    }
+    __syncthreads();
+    if (col >= rb) continue;
+    for (int i = 0; i < m; i += 8) {
+      uint4 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < m && from[i + j] >= 0) w[j] = *reinterpret_cast<const uint4*>(base + from[i + j] * rb);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < m && from[i + j] >= 0) *reinterpret_cast<uint4*>(base + to[i + j] * rb) = w[j];
+    }
+  }
+}
+
+__global__ void cut_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
+                           const int32_t* accepted, const int32_t* slots, int* err) {
+  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, blockIdx.x, err);
+  if (!k.ok) return;
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) c.lens[k.slot] = k.base + k.count;
+  release(c, k.slot, pages_of(k.base + k.count, c.page_size), pages_of(k.len, c.page_size), err);
+}
+
+}  // namespace
+
+static cudaError_t grant_smem(const void* kern, size_t smem) {
+  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))
+                          : cudaSuccess;
+}
+
+cudaError_t launch_alloc(const attn_cache_t& c, const int32_t* slots, const int32_t* want, int n, int32_t* granted,
+                         int* err, cudaStream_t st) {
+  const size_t smem = (static_cast<size_t>(c.slots) + n) * sizeof(int);
+  const cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<false>), smem);
+  if (e != cudaSuccess) return e;
+  grant_kernel<false><<<1, kBlock, smem, st>>>(c, slots, want, n, granted, nullptr, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_free(const attn_cache_t& c, const int32_t* slots, int n, int* err, cudaStream_t st) {
+  free_kernel<<<n, 128, 0, st>>>(c, slots, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fork(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int32_t* granted,
+                        void* ws, int* err, cudaStream_t st) {
+  const size_t smem = (static_cast<size_t>(c.slots) + n) * sizeof(int);
+  cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<true>), smem);
+  if (e != cudaSuccess) return e;
+  ForkItem* items = static_cast<ForkItem*>(ws);
+  grant_kernel<true><<<1, kBlock, smem, st>>>(c, src, dst, n, granted, items, err);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  fork_kernel<<<dim3(n, 1 + 2 * c.layers), 256, 0, st>>>(c, items, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_copy(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int* err, cudaStream_t st) {
+  // A block reads the whole list of destinations, so there are no more blocks than fill
+  // the device: about 4096, in pieces of at least 4 KB (page_size >= 16 rows of 64 bytes
+  // or more divide evenly into the powers of two used here).
+  const int64_t bytes = static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2) * c.page_size;
+  int chunks = 1;
+  while (chunks < 16 && bytes / (2 * chunks) >= 4096 && static_cast<int64_t>(n) * c.layers * 2 * chunks < 4096) chunks *= 2;
+  int parts = 4096 / n;
+  if (parts > c.layers * 2 * chunks) parts = c.layers * 2 * chunks;
+  if (parts < 1) parts = 1;
+  copy_kernel<<<dim3(n, parts), 256, 0, st>>>(c, src, dst, n, chunks, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_compact(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
+                           const int32_t* accepted, const int32_t* slots, int B, int* err, cudaStream_t st) {
+  const int64_t words = static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2) / 16;
+  const int threads = words >= 256 ? 256 : static_cast<int>((words + 31) / 32 * 32);
+  const int z = static_cast<int>((words + threads - 1) / threads);
+  compact_kernel<<<dim3(B, 2 * c.layers, z), threads, 0, st>>>(c, cu_q, path, width, accepted, slots, err);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cut_kernel<<<B, 128, 0, st>>>(c, cu_q, path, width, accepted, slots, err);
+  return cudaGetLastError();
+}
+
+}  // namespace attn
