@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libattn.so")
 SOURCES = ["attn_api.cu", "attn_fwd_sm100.cu", "attn_bwd_sm100.cu", "selftest_sm100.cu",
            "attn_noalloc.cu", "rope_sm100.cu", "cache_pages.cu", "attn_tree_sm100.cu", "cache_api.cu"]
 HEADERS = ["attn_fwd_sm100.h", "attn_bwd_sm100.h", "attn_internal.h", "sm100_ptx.cuh", "softmax_math.cuh",
-           "exp2_poly.h", "cache_ops.h"]
+           "exp2_poly.h", "cache_ops.h", "cache_ptx.cuh"]
 PUBLIC_HEADERS = [os.path.join(ROOT, "include", h) for h in ("attn.h", "attn_cache.h", "attn_selftest.h")]
 NVCC = os.environ.get("NVCC", "nvcc")
 # Extra nvcc flags (e.g. -DATTN_P_SPLIT=4 to change how P~ is handed to the PV product).

@@ -213,6 +213,18 @@ attn_status_t prepare_device(int** err, int* sms) {
   return ATTN_OK;
 }
 
+bool make_tensor_map(CUtensorMap* m, const void* ptr, int esz, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box, int swizzle_bytes) {
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  cuuint64_t d[5], s[4];
+  for (int i = 0; i < rank; ++i) d[i] = dims[i];
+  for (int i = 0; i + 1 < rank; ++i) s[i] = strides[i];
+  return g_encode(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                  const_cast<void*>(ptr), d, s, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 attn_status_t load_tensor_map_encoder() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_encode) return ATTN_OK;

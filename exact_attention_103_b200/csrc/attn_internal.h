@@ -54,6 +54,11 @@ attn_status_t load_tensor_map_encoder();
 // Prepares the current device (as every entry point does on its first call) and gives
 // its error word and SM count.
 attn_status_t prepare_device(int** err, int* sms);
+// A tiled view of `rank` dimensions (innermost first; `strides` in bytes from dimension 1 on) of
+// 16-bit floats (esz 2) or bytes (esz 1), with 128- or 64-byte swizzle.  Call after
+// prepare_device.
+bool make_tensor_map(CUtensorMap* m, const void* ptr, int esz, int rank, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box, int swizzle_bytes);
 // Records `message` as the calling thread's last error and returns `s`.
 attn_status_t report(attn_status_t s, const char* message);
 

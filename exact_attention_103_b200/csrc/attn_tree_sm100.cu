@@ -1,88 +1,1038 @@
-// attn_tree_sm100.cu -- exact attention of new tokens over the paged cache.
+// attn_tree_sm100.cu -- exact attention of each sequence's newest (drafted) tokens over
+// the paged cache, for B200 (sm_100a): tree_kernel, and combine_kernel for the rows whose keys
+// were split over several CTAs.
 //
-// One warp per (token, query head): keys one by one, each lane holding d / 32 values of the
-// head, with the running maximum and sum of the softmax in fp32.
+// The mathematics is the forward kernel's (attn_fwd_sm100.cu): O = sum_j 2^(x_j - m) v_j /
+// sum_j 2^(x_j - m), x = scale log2(e) q.k, one pass over the keys with a running
+// maximum m per row, rescaled only when it grows by more than tau.
+//
+// What bounds it: a cache is read once per step, 2 d values per (token, cache head), for
+// 4 d flops per query row: below about 128 query rows per cache head the copies from HBM bound
+// it, above the tensor cores.  Hence:
+//  - The query heads that share a cache head, and all drafted tokens, are packed into the rows
+//    of one item: row r of a 128-row tile is token r / G, head r % G of the group (G = Hq /
+//    heads), so K and V are read once for all of them.
+//  - Work is dealt in equal numbers of 128-key tiles: the tiles of all (sequence, cache head, row
+//    pair) items form one list, and CTA c of the grid takes the c-th equal part.  One long
+//    sequence fills every SM as well as many short ones do.  A part that begins or ends
+//    inside an item leaves its rows' unnormalised O (fp32), maximum and sum in the workspace; a
+//    CTA leaves at most two of those.  combine_kernel joins them in a fixed order.
+//  - An item of up to 128 rows runs its key tiles alternately through the two softmax
+//    warpgroups (tile j in stream j % 2, each with its own S and O in TMEM, joined at the
+//    end), so that one tile's softmax overlaps the other's products.  An item of 129 to 256 rows
+//    gives each warpgroup its own 128 rows of every key tile.
+//
+// E4M3 caches: the keys and values go to the tensor cores as they are (kind::f8f6f4), and the
+// other operand of each product is split into two E4M3 terms, hi + lo, which keeps bf16's
+// precision: a bf16 query scaled by a power of two (its row's largest value in [128, 256)) is
+// hi + lo exactly down to 2^-9 of that scale, and hi + lo holds P~ to 2^-8 (the first term keeps 4
+// significant bits, the second 4 more).  Each costs one more product, at twice bf16's rate.
+//
+// Warp roles (384 threads): 0-3 and 4-7 softmax, correction and epilogue of streams 0 and 1;
+// 8 TMA producer; 9 TMEM owner and tcgen05.mma issuer; 10 and 11 write the split queries of
+// E4M3 caches (idle otherwise).  Every wait is bounded; on expiry the CTA stops, drains its
+// copies and products, frees TMEM and returns.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include "attn_internal.h"
 #include "cache_ops.h"
+#include "cache_ptx.cuh"
 
 namespace attn {
 namespace {
 
+constexpr int kThreads = 384;
+constexpr int kBM = 128;  // rows of a tile
+constexpr int kBN = 128;  // keys of a tile
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+enum TreeSite : int {  // wait sites of the device error word (16..30)
+  kSiteTQFull = 16, kSiteTQEmpty, kSiteTKvFull, kSiteTKvEmpty, kSiteTSFull, kSiteTPFull, kSiteTOFull, kSiteTMerge,
+  kSiteTDrain
+};
+__host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
+
+struct TreeParams {
+  __nv_bfloat16* o;
+  float* lse;
+  const __nv_bfloat16* q;
+  const int32_t *cu, *slots, *page_table, *lens;
+  const uint8_t* mask;
+  int mask_width;
+  int Hq, heads, G, B, T;
+  int nslots, max_pages, pages, page_shift;
+  int layer_row;   // first row of the layer in the tensor maps
+  int rows;        // rows of the tensor maps: a copy from there on gives zeros
+  int box_rows;    // rows of one K/V copy: min(page size, 128)
+  int tpt;         // tokens of a 128-row tile: 128 / G
+  float scale_log2, o_scale, tau, p_shift;
+  float* part;     // [grid][2][256][D] unnormalised O
+  float2* stat;    // [grid][2][256] (maximum in log2 units, sum)
+  int4* head;      // [grid] the item whose first tiles this CTA left unfinished
+  int* err;
+};
+
+// head[c]: x = global row of its first token (-1: none), y = cache head, z = tokens, w = last CTA.
+
 template <int D, bool F8>
-__global__ void __launch_bounds__(128) tree_kernel(const __grid_constant__ TreeArgs a) {
-  constexpr int E = D / 32;
-  const attn_cache_t& c = a.cache;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(a.T) * a.Hq) return;
-  const int t = static_cast<int>(w / a.Hq), h = static_cast<int>(w % a.Hq);
-  int b = -1;
-  for (int i = 0; i < a.B; ++i)
-    if (a.cu[i] <= t && t < a.cu[i + 1]) b = i;
-  if (b < 0) return;
-  const int n = a.cu[b + 1] - a.cu[b], local = t - a.cu[b];
-  const int slot = a.slots ? a.slots[b] : b;
-  if (slot < 0 || slot >= c.slots) {
-    record_invalid(a.err, kSiteSlot);
-    return;
+struct Layout {
+  static constexpr int ESZ = F8 ? 1 : 2;
+  static constexpr int ROWB = D * ESZ < 128 ? D * ESZ : 128;  // bytes of a row in one swizzled chunk
+  static constexpr int NCHUNK = D * ESZ / ROWB;
+  static constexpr int CHUNK = kBM * ROWB;
+  static constexpr int TILE = NCHUNK * CHUNK;
+  static constexpr int CELEMS = ROWB / ESZ;  // values of a row in a chunk
+  static constexpr int KSTEP = 32 / ESZ;     // values of a K step of the products
+  static constexpr int NSTAGE = TILE >= 32768 ? 4 : 8;
+  static constexpr int QTILE = F8 ? 2 * TILE : TILE;  // E4M3: hi, then lo
+  static constexpr int Q_OFF = 0;
+  static constexpr int KV_OFF = 2 * QTILE;
+  static constexpr int ML_OFF = KV_OFF + NSTAGE * TILE;      // float2 [2][128]: (m, l) of the two streams
+  static constexpr int QS_OFF = ML_OFF + 2 * kBM * 8;        // float [2][128]: 1 / scale of the split queries
+  static constexpr int BAR_OFF = QS_OFF + 2 * kBM * 4;
+  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 10, B_ML = 11, B_EPI = 12,
+                       B_DRAIN = 13, B_KVFULL = 14, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int TABLE_OFF = MISC_OFF + 128;
+  static constexpr int TM_S0 = 0, TM_S1 = 128, TM_O0 = 256, TM_O1 = 256 + D;
+};
+
+__device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// One CTA's stretch of an item: key tiles [j0, j1) of kvt.
+struct Seg {
+  int h, tok0, nt;        // cache head; first token (of the sequence) and number of tokens
+  int n, ctx, len, slot;  // the sequence: drafted tokens, context, tokens in the cache, slot
+  int q0;                 // its first row of q
+  int j0, j1, kvt;
+  bool two;               // more than one row tile
+};
+
+// The list of work, decoded alike by every role.  Tables in shared memory, per sequence:
+// cum (tiles before it), first row of q, slot, tokens in the cache.
+struct List {
+  const int *cum, *cu, *slot, *len;
+  int B, heads, tpt;
+  bool masked;
+
+  // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
+  // than itself.
+  __device__ __forceinline__ int tiles(int n, int length, int rt) const {
+    const int end = masked ? n : min((rt + 1) * 2 * tpt, n);
+    return (length - n + end + kBN - 1) / kBN;
   }
-  const int len = c.lens[slot];
-  if (len < n || len > static_cast<int64_t>(c.max_pages) * c.page_size || (a.mask && n > a.mask_width)) {
-    record_invalid(a.err, kSiteLength);
-    return;
-  }
-  const int hk = h / (a.Hq / c.heads);
-  float q[E], o[E] = {};
-  for (int e = 0; e < E; ++e)
-    q[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[(static_cast<int64_t>(t) * a.Hq + h) * D + lane * E + e]);
-  const float ks = F8 ? c.k_scale : 1.f, vs = F8 ? c.v_scale : 1.f;
-  auto value = [&](const void* base, int64_t at) -> float {
-    if constexpr (F8) return static_cast<float>(static_cast<const __nv_fp8_e4m3*>(base)[at]);
-    else return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
-  };
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < len; ++j) {
-    const int jl = j - (len - n);
-    if (jl >= 0 && (a.mask ? a.mask[static_cast<int64_t>(t) * a.mask_width + jl] == 0 : jl > local)) continue;
-    const int page = c.page_table[static_cast<int64_t>(slot) * c.max_pages + j / c.page_size];
-    if (page < 0 || page >= c.pages) {
-      record_invalid(a.err, kSitePage);
-      return;
+  __device__ __forceinline__ Seg at(int x, int end) const {
+    int lo = 0, hi = B - 1;  // the sequence with cum[b] <= x < cum[b + 1]
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (cum[mid + 1] > x) hi = mid; else lo = mid + 1;
     }
-    const int64_t at = (((static_cast<int64_t>(a.layer) * c.pages + page) * c.page_size + j % c.page_size) * c.heads + hk) * D + lane * E;
-    float s = 0.f;
-    for (int e = 0; e < E; ++e) s += q[e] * value(c.k, at + e);
-    for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale * ks;
-    const float top = fmaxf(m, s);
-    const float old = m == -INFINITY ? 0.f : expf(m - top), p = expf(s - top);
-    m = top;
-    l = l * old + p;
-    for (int e = 0; e < E; ++e) o[e] = o[e] * old + p * value(c.v, at + e);
+    Seg s;
+    s.q0 = cu[lo];
+    s.n = cu[lo + 1] - s.q0;
+    s.slot = slot[lo];
+    s.len = len[lo];
+    s.ctx = s.len - s.n;
+    const int per_head = (cum[lo + 1] - cum[lo]) / heads;
+    int r = x - cum[lo];
+    s.h = r / per_head;
+    r -= s.h * per_head;
+    int rt = 0, kv = tiles(s.n, s.len, 0);
+    while (r >= kv) {
+      r -= kv;
+      kv = tiles(s.n, s.len, ++rt);
+    }
+    s.tok0 = rt * 2 * tpt;
+    s.nt = min(2 * tpt, s.n - s.tok0);
+    s.two = s.nt > tpt;
+    s.kvt = kv;
+    s.j0 = r;
+    s.j1 = min(kv, r + end - x);
+    return s;
   }
-  for (int e = 0; e < E; ++e)
-    static_cast<__nv_bfloat16*>(a.o)[(static_cast<int64_t>(t) * a.Hq + h) * D + lane * E + e] = __float2bfloat16(l > 0.f ? o[e] / l * vs : 0.f);
-  if (lane == 0) a.lse[static_cast<int64_t>(h) * a.T + t] = l > 0.f ? m + logf(l) : -INFINITY;
+};
+
+// The order of K and V tiles in the ring.  The products run as units: S(u) and P~V(u), with
+// S two units ahead.  One row tile: unit u is key tile u, so K runs two tiles ahead of V; two
+// row tiles: units 2j and 2j + 1 are key tile j, K runs one ahead.
+__device__ __forceinline__ int k_pos(int j, int lead) { return j + max(0, j - lead + 1); }
+__device__ __forceinline__ int v_pos(int j, int n, int lead) { return j + min(n, j + lead); }
+
+__device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+  return true;
+}
+
+// x rounded to 4 significant bits (Veltkamp's splitting: t = (2^20 + 1) x, t - (t - x)), in
+// roundings that must not be contracted to an fma.
+__device__ __forceinline__ float upper4(float x) {
+  const float t = __fmul_rn(x, 1048577.f);
+  return __fsub_rn(t, __fsub_rn(t, x));
+}
+
+// Bits [0, k) of word g of a 128-bit set of columns.
+__device__ __forceinline__ uint32_t below(int k, int g) {
+  k -= 32 * g;
+  return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u;
+}
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+  using Lay = Layout<D, F8>;
+  constexpr int NS = Lay::NSTAGE;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int i) -> uint32_t { return sb + Lay::BAR_OFF + 8 * i; };
+  uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::MISC_OFF);
+  // misc[0] TMEM base, misc[1] abort flag, misc[4..16) sums of the warps
+  int* tab = reinterpret_cast<int*>(smem + Lay::TABLE_OFF);
+  int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(Lay::B_QFULL + s), F8 ? 2 : 1);
+      mbar_init(bar(Lay::B_QEMPTY + s), F8 ? 9 : 1);  // E4M3: and the softmax warps, with the row scales
+      mbar_init(bar(Lay::B_SFULL + s), 1);
+      for (int h = 0; h < 2; ++h) mbar_init(bar(Lay::B_PFULL + 2 * s + h), 4);
+    }
+    mbar_init(bar(Lay::B_OFULL), 1);
+    mbar_init(bar(Lay::B_ML), 8);
+    mbar_init(bar(Lay::B_EPI), 8);
+    mbar_init(bar(Lay::B_DRAIN), 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(Lay::B_KVFULL + i), 1);
+      mbar_init(bar(Lay::B_KVEMPTY + i), 1);
+    }
+    misc[1] = 0u;
+    fence_barrier_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(sb + Lay::MISC_OFF, 512);
+    tmem_relinquish();
+  }
+  List list;
+  list.cum = t_cum;
+  list.cu = t_cu;
+  list.slot = t_slot;
+  list.len = t_len;
+  list.B = p.B;
+  list.heads = p.heads;
+  list.tpt = p.tpt;
+  list.masked = p.mask != nullptr;
+  {
+    // The tiles of each sequence and their prefix sum; a thread takes consecutive sequences.
+    const int per = ceil_div(p.B, kThreads);
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
+    int sum = 0, broken = 0;
+    for (int b = b0; b < b1; ++b) {
+      const int first = __ldg(p.cu + b), n = __ldg(p.cu + b + 1) - first;
+      const int slot = p.slots ? __ldg(p.slots + b) : b;
+      int len = 0, work = 0;
+      if (n < 0 || first < 0 || n > p.T - first) {
+        broken = 1;  // nothing of the batch can be told apart
+      } else if (n != 0) {
+        int bad = 0;
+        if (slot < 0 || slot >= p.nslots) {
+          bad = kSiteSlot;
+        } else {
+          len = __ldg(p.lens + slot);
+          if (len < n || len > (static_cast<int64_t>(p.max_pages) << p.page_shift) || (p.mask && n > p.mask_width))
+            bad = kSiteLength;
+        }
+        if (bad) {
+          record_invalid(p.err, bad);
+        } else {
+          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.tiles(n, len, rt);
+          work *= p.heads;
+        }
+      }
+      t_cu[b] = first;
+      t_slot[b] = slot;
+      t_len[b] = len;
+      sum += work;
+      t_cum[b + 1] = sum;
+    }
+    if (threadIdx.x == 0) {
+      t_cum[0] = 0;
+      t_cu[p.B] = __ldg(p.cu + p.B);
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) misc[4 + warp] = static_cast<uint32_t>(incl);
+    if (__syncthreads_or(broken)) {
+      if (threadIdx.x == 0) record_invalid(p.err, kSiteLength);
+      for (int b = b0; b < b1; ++b) t_cum[b + 1] = 0;
+      if (lane == 0) misc[4 + warp] = 0u;
+      incl = sum = 0;
+      __syncthreads();
+    }
+    int before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += static_cast<int>(misc[4 + w]);
+    for (int b = b0; b < b1; ++b) t_cum[b + 1] += before;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc[0];
+  const int total = t_cum[p.B];
+  const int ctas = min(static_cast<int>(gridDim.x), total);  // CTAs with work: one tile at least
+  const int cta = static_cast<int>(blockIdx.x);
+  const int x0 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta) * total / ctas) : 0;
+  const int x1 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta + 1) * total / ctas) : 0;
+  WaitCtl wc;
+  wc.abort = reinterpret_cast<volatile uint32_t*>(misc + 1);
+  wc.err = p.err;
+  wc.limit_ns = kTimeoutNs;
+  auto wait = [&](int b, uint32_t parity, int site) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, wc, timeout_code(site)));
+  };
+
+  // 4 x 32 x (168 - 120) registers released by warpgroup 2, 8 x 32 x (192 - 168) taken.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n" ::: "memory");
+    // ------------------------------------------------------------ softmax
+    // Stream s = warp / 4; warp w owns TMEM lanes 32(w%4)..+31, one row per thread.
+    const int s = warp >> 2, wq = warp & 3;
+    const int r = wq * 32 + lane;
+    const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t t_s = tmem + lane_bits + (s ? Lay::TM_S1 : Lay::TM_S0);
+    const uint32_t t_o = tmem + lane_bits + (s ? Lay::TM_O1 : Lay::TM_O0);
+    const int tl = r / p.G, g = r - tl * p.G;  // token of the tile, head of the group
+    float2* ml = reinterpret_cast<float2*>(smem + Lay::ML_OFF);
+    uint32_t s_phase = 0, o_phase = 0, m_phase = 0, e_phase = 0;
+    int nq = 0;  // row tiles of q taken so far
+    bool ok = true;
+    for (int x = x0; x < x1 && ok;) {
+      const Seg it = list.at(x, x1);
+      x += it.j1 - it.j0;
+      const int first = it.two ? s * p.tpt : 0;  // this stream's first token of the item
+      const int mine = it.two ? (s ? it.nt - p.tpt : p.tpt) : it.nt;
+      const int tok = it.tok0 + first + tl;      // this row's token of the sequence
+      const bool valid = tl < mine;
+      const bool busy = wq * 32 < mine * p.G;    // the warp has a valid row
+      const int jstep = it.two ? 1 : 2;
+      float sl = p.scale_log2;
+      if constexpr (F8) {
+        const int mine_q = nq + (it.two ? s : 0);
+        ok = wait(Lay::B_QFULL + (mine_q & 1), (mine_q >> 1) & 1, kSiteTQFull);
+        if (!ok) break;
+        sl = p.scale_log2 * reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(Lay::B_QEMPTY + (nq & 1)));
+          if (it.two) mbar_arrive(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
+        }
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int j = it.j0 + (it.two ? 0 : s); j < it.j1; j += jstep) {
+        ok = wait(Lay::B_SFULL + s, s_phase, kSiteTSFull);
+        if (!ok) break;
+        s_phase ^= 1u;
+        tc_fence_after();
+        any = true;
+        auto release = [&](int half) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Lay::B_PFULL + 2 * s + half));
+        };
+        if (!busy) {  // nothing to compute: the rows of P~ that stay behind are never read
+          release(0);
+          release(1);
+          continue;
+        }
+        uint32_t sa[64], sz[64];
+        tmem_ld_x64(t_s, sa);
+        tmem_ld_x64_async(t_s + 64, sz);
+        const int kb = j * kBN;
+        const bool part = kb + kBN > it.ctx;  // the tile holds drafted tokens, or ends behind them
+        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
+        if (part) {
+          if (p.mask == nullptr) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vis[c] = below(it.ctx + tok + 1 - kb, c);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vis[c] = below(it.ctx - kb, c);
+            // The mask rows of the warp's tokens, 32 columns per load, 4 tokens at a time.
+            const int t_lo = (wq * 32) / p.G, t_hi = min((wq * 32 + 31) / p.G, mine - 1);
+            const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first) * p.mask_width;
+            const int col = kb + lane - it.ctx;
+            for (int t0 = t_lo; t0 <= t_hi; t0 += 4) {
+              uint8_t w[4][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const int jl = col + 32 * c;
+                  w[i][c] = (t0 + i <= t_hi && jl >= 0 && jl < it.n)
+                                ? __ldg(rows + static_cast<int64_t>(t0 + i) * p.mask_width + jl)
+                                : 0;
+                }
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t bits = __ballot_sync(0xffffffffu, w[i][c] != 0);
+                  if (t0 + i == tl) vis[c] |= bits;
+                }
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((vis[c >> 5] >> (c & 31)) & 1u)) sa[c] = __float_as_uint(-INFINITY);
+        }
+        float m4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m4[i] = fmax3(__uint_as_float(sa[i]), __uint_as_float(sa[i + 4]), __uint_as_float(sa[i + 8]));
+#pragma unroll
+        for (int c = 12; c < 60; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m4[i] = fmax3(m4[i], __uint_as_float(sa[c + i]), __uint_as_float(sa[c + 4 + i]));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(sa[60 + i]));
+        tmem_wait_ld_x64(sz);
+        if (part) {
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (!((vis[2 + (c >> 5)] >> (c & 31)) & 1u)) sz[c] = __float_as_uint(-INFINITY);
+        }
+#pragma unroll
+        for (int c = 0; c < 64; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m4[i] = fmax3(m4[i], __uint_as_float(sz[c + i]), __uint_as_float(sz[c + 4 + i]));
+        const float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sl;
+        bool need = false;
+        float alpha = 1.f;
+        if (m_ref == -INFINITY) {  // the first tile with a key that this row sees
+          m_ref = m_tile;
+        } else if (m_tile - m_ref > p.tau) {
+          need = valid;
+          alpha = fast_exp2(m_ref - m_tile);
+          m_ref = m_tile;
+          l *= alpha;
+        }
+        float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+        if constexpr (F8) nm += p.p_shift;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        auto rescale = [&]() {
+          // O of this stream is stable: the commit that signalled S also covers its last P~V.
+          if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld_x32(t_o + 32 * c, ov);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tmem_st_x32(t_o + 32 * c, ov);
+            }
+          }
+        };
+        auto exps = [&](int c, float& a, float& e) {  // column pair c (keys 2c, 2c + 1)
+          const uint32_t y0 = c < 32 ? sa[2 * c] : sz[2 * c - 64];
+          const uint32_t y1 = c < 32 ? sa[2 * c + 1] : sz[2 * c - 63];
+          ffma2_bc(a, e, __uint_as_float(y0), __uint_as_float(y1), sl, nm);
+          a = fast_exp2(a);
+          e = fast_exp2(e);
+          if (c & 1) fadd2_acc(ls[2], ls[3], a, e);
+          else fadd2_acc(ls[0], ls[1], a, e);
+        };
+        if constexpr (!F8) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int cc = 0; cc < 32; ++cc) {
+              float a, e;
+              exps(32 * half + cc, a, e);
+              pk[cc] = pack_bf16x2(a, e);
+            }
+            tmem_st_x32(t_s + 32 * half, pk);
+            if (half == 0) rescale();
+            release(half);
+          }
+        } else {
+          // P~ = hi + lo; the conversion of hi is exact while it is a normal E4M3 number.
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+#pragma unroll
+            for (int cc = 0; cc < 32; ++cc) {
+              float a, e;
+              exps(32 * half + cc, a, e);
+              const float ha = upper4(a), he = upper4(e);
+              const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(a - ha, e - he);
+              if (cc & 1) {
+                hi[cc >> 1] |= wh << 16;
+                lo[cc >> 1] |= wl << 16;
+              } else {
+                hi[cc >> 1] = wh;
+                lo[cc >> 1] = wl;
+              }
+            }
+            tmem_st_x16(t_s + 16 * half, hi);
+            tmem_st_x16(t_s + 32 + 16 * half, lo);
+            if (half == 0) rescale();
+            release(half);
+          }
+        }
+        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      }
+      nq += it.two ? 2 : 1;
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      // Two row tiles: each warpgroup writes its own rows.  One: the streams' O are joined, and
+      // each warpgroup writes half the columns.
+      float a0 = 1.f, a1 = 0.f;  // weights of this stream's O and the other's
+      if (!it.two) {
+        ml[s * kBM + r] = make_float2(m_ref, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::B_ML));
+        ok = wait(Lay::B_ML, m_phase, kSiteTMerge);
+        if (!ok) break;
+        m_phase ^= 1u;
+        const float2 other = ml[(s ^ 1) * kBM + r];
+        const float m = fmaxf(m_ref, other.x);
+        a0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
+        a1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - m);
+        l = l * a0 + other.y * a1;
+        m_ref = m;
+      }
+      ok = wait(Lay::B_OFULL, o_phase, kSiteTOFull);
+      if (!ok) break;
+      o_phase ^= 1u;
+      tc_fence_after();
+      const bool whole = it.j0 == 0 && it.j1 == it.kvt;
+      if (busy) {
+        const int64_t row = static_cast<int64_t>(it.q0 + tok) * p.Hq + it.h * p.G + g;
+        const int64_t slot_row = (static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0)) * (2 * kBM) + (it.two ? s * kBM : 0) + r;
+        const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
+        // Columns of this warpgroup; a stream that took no tile has nothing in its O.
+        const int c_lo = it.two ? 0 : s * (D / 64), c_hi = it.two ? D / 32 : (s + 1) * (D / 64);
+        const bool use_own = any, use_other = !it.two && (s ? true : it.j1 - it.j0 > 1);
+        const uint32_t t_x = tmem + lane_bits + (s ? Lay::TM_O0 : Lay::TM_O1);
+        for (int c = c_lo; c < c_hi; ++c) {
+          uint32_t ov[32];
+          float v[32];
+          if (use_own) {
+            tmem_ld_x32(t_o + 32 * c, ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * a0;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+          if (use_other) {
+            tmem_ld_x32(t_x + 32 * c, ov);
+            // weight 0 also where the other stream's O was never a number
+            if (a1 != 0.f) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), a1, v[i]);
+            }
+          }
+          if (valid && whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
+                                  pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                  pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                                  pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+          } else if (valid) {
+            float4* dst = reinterpret_cast<float4*>(p.part + slot_row * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        if (valid && (it.two || s == 0)) {
+          if (whole) {
+            p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] =
+                l > 0.f ? (m_ref + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
+          } else {
+            p.stat[slot_row] = make_float2(m_ref, l);
+          }
+        }
+      }
+      // The next item's P~V may write either O only when both warpgroups have read them, and
+      // neither warpgroup runs an item ahead of the other.
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Lay::B_EPI));
+      ok = wait(Lay::B_EPI, e_phase, kSiteTMerge);
+      e_phase ^= 1u;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n" ::: "memory");
+    if (warp == 8) {
+      // ----------------------------------------------------------- producer
+      if (elect_one()) {
+        tma_prefetch_map(&tm_q);
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+      }
+      __syncwarp();
+      const uint64_t pol = l2_policy_evict_normal();
+      uint32_t n_ld = 0;
+      int nq = 0;
+      bool ok = true;
+      const int per_tile = kBN / p.box_rows;  // copies of a full tile
+      for (int x = x0; x < x1 && ok;) {
+        const Seg it = list.at(x, x1);
+        x += it.j1 - it.j0;
+        if constexpr (!F8) {
+          for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
+            const int slot = nq & 1;
+            if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
+            if (!ok) break;
+            if (elect_one()) {
+              mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * p.tpt * p.G * Lay::ROWB);
+#pragma unroll
+              for (int c = 0; c < Lay::NCHUNK; ++c)
+                tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, &tm_q, bar(Lay::B_QFULL + slot),
+                            c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+        }
+        const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
+        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
+        // Lane i's copy of a tile: rows box_rows * i ..; its page is looked up one tile ahead.
+        auto page_at = [&](int j) -> int {
+          const int pos = (it.j0 + j) * kBN + lane * p.box_rows;
+          return (j < nj && lane < per_tile && pos < it.len) ? __ldg(row + (pos >> p.page_shift)) : 0;
+        };
+        int next_k = page_at(0), next_v = next_k;
+        int kj = 0, vj = 0;
+        while (vj < nj && ok) {
+          const bool is_k = kj < nj && kj < vj + lead;
+          const int j = is_k ? kj : vj;
+          const int page = is_k ? next_k : next_v;
+          if (is_k) next_k = page_at(++kj);
+          else next_v = page_at(++vj);
+          const uint32_t slot = n_ld % NS;
+          if (n_ld >= static_cast<uint32_t>(NS))
+            ok = wait(Lay::B_KVEMPTY + slot, ((n_ld / NS) - 1) & 1u, kSiteTKvEmpty);
+          if (!ok) break;
+          const int kb = (it.j0 + j) * kBN;
+          const int copies = min(per_tile, ceil_div(it.len - kb, p.box_rows));
+          if (lane == 0) mbar_arrive_expect_tx(bar(Lay::B_KVFULL + slot), copies * p.box_rows * Lay::ROWB * Lay::NCHUNK);
+          __syncwarp();
+          if (lane < copies) {
+            const int pos = kb + lane * p.box_rows;
+            int at = p.rows;
+            if (page >= 0 && page < p.pages) at = p.layer_row + (page << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+            else record_invalid(p.err, kSitePage);
+            const uint32_t dst = sb + Lay::KV_OFF + slot * Lay::TILE + lane * p.box_rows * Lay::ROWB;
+#pragma unroll
+            for (int c = 0; c < Lay::NCHUNK; ++c)
+              tma_load_3d(dst + c * Lay::CHUNK, is_k ? &tm_k : &tm_v, bar(Lay::B_KVFULL + slot), c * Lay::CELEMS, it.h, at, pol);
+          }
+          __syncwarp();
+          ++n_ld;
+        }
+      }
+      // Every copy has landed before the CTA may exit.
+      const uint32_t first = n_ld > static_cast<uint32_t>(NS) ? n_ld - NS : 0u;
+      for (uint32_t n = first; n < n_ld; ++n) drain_wait(bar(Lay::B_KVFULL + n % NS), (n / NS) & 1u, kDrainLimitNs);
+      if constexpr (!F8) {
+        for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n) drain_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, kDrainLimitNs);
+      }
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMA
+      constexpr uint32_t idesc_s = F8 ? idesc_e4m3_f32(kBM, kBN, 0, 0) : idesc_bf16_f32(kBM, kBN, 0, 0);
+      constexpr uint32_t idesc_o = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
+      constexpr bool SW64 = Lay::ROWB == 64;
+      auto k_desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
+      uint32_t n_ld = 0, p_phase0 = 0, p_phase1 = 0;
+      int nq = 0;
+      bool ok = true;
+      for (int x = x0; x < x1 && ok;) {
+        const Seg it = list.at(x, x1);
+        x += it.j1 - it.j0;
+        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2, units = it.two ? 2 * nj : nj;
+        for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k)
+          ok = wait(Lay::B_QFULL + ((nq + k) & 1), ((nq + k) >> 1) & 1, kSiteTQFull);
+        if (!ok) break;
+        tc_fence_after();
+        auto issue_s = [&](int u) {
+          const int j = it.two ? u >> 1 : u, s = u & 1;
+          const uint32_t n = n_ld + k_pos(j, lead), slot = n % NS;
+          if (!it.two || s == 0) {
+            ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+            if (!ok) return;
+            tc_fence_after();
+          }
+          const int qslot = (nq + (it.two ? s : 0)) & 1;
+          const uint32_t tS = tmem + (s ? Lay::TM_S1 : Lay::TM_S0);
+          const uint32_t qbase = sb + Lay::Q_OFF + qslot * Lay::QTILE, kbase = sb + Lay::KV_OFF + slot * Lay::TILE;
+          if (elect_one()) {
+            const uint64_t db0 = k_desc(kbase);
+#pragma unroll
+            for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+              const uint64_t da0 = k_desc(qbase + term * Lay::TILE);
+              constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
+#pragma unroll
+              for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
+                const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
+                const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
+                if constexpr (F8) mma_ss_f8(tS, desc_add(da0, off), desc_add(db0, off), idesc_s, acc);
+                else mma_ss(tS, desc_add(da0, off), desc_add(db0, off), idesc_s, acc);
+              }
+            }
+            tc_commit(bar(Lay::B_SFULL + s));
+            if (!it.two || s == 1) tc_commit(bar(Lay::B_KVEMPTY + slot));
+            // the row tile of q is free after its last S
+            if (it.two ? j == nj - 1 : u == units - 1) tc_commit(bar(Lay::B_QEMPTY + qslot));
+          }
+          __syncwarp();
+        };
+        issue_s(0);
+        if (ok && units > 1) issue_s(1);
+        for (int u = 0; u < units && ok; ++u) {
+          const int j = it.two ? u >> 1 : u, s = u & 1;
+          const uint32_t n = n_ld + v_pos(j, nj, lead), slot = n % NS;
+          const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE;
+          const int left = it.len - (it.j0 + j) * kBN;  // keys of the tile inside the sequence, or more
+          const int steps = min(kBN / Lay::KSTEP, ceil_div(left, Lay::KSTEP));
+          if (!it.two || s == 0) {
+            ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+            if (!ok) break;
+            tc_fence_after();
+            if (left < steps * Lay::KSTEP) {
+              // Rows behind the sequence's end that the last K step would multiply: whatever
+              // the page holds there must not meet the zero weights.
+              constexpr int U = Lay::ROWB / 16;
+              const int rows = steps * Lay::KSTEP - left;
+              for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
+                const int c = i / (rows * U), w = i - c * rows * U;
+                *reinterpret_cast<uint4*>(smem + Lay::KV_OFF + slot * Lay::TILE + c * Lay::CHUNK + left * Lay::ROWB + w * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+          }
+          const uint32_t tS = tmem + (s ? Lay::TM_S1 : Lay::TM_S0), tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
+          uint32_t& ph = s ? p_phase1 : p_phase0;
+          const bool start = u < 2;  // the stream's first product
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = wait(Lay::B_PFULL + 2 * s + half, ph, kSiteTPFull);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              constexpr int NK = kBN / Lay::KSTEP;
+              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
+#pragma unroll
+              for (int kk = half * NK / 2; kk < (half + 1) * NK / 2; ++kk) {
+                if (kk >= steps) continue;
+                const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
+                const uint32_t acc = (!start || kk > 0) ? 1u : 0u;
+                if constexpr (F8) {
+                  mma_ts_f8(tO, tS + kk * 8, dv, idesc_o, acc);
+                  mma_ts_f8(tO, tS + 32 + kk * 8, dv, idesc_o, 1u);
+                } else {
+                  mma_ts(tO, tS + kk * 8, dv, idesc_o, acc);
+                }
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          ph ^= 1u;
+          if (elect_one()) {
+            if (!it.two || s == 1) tc_commit(bar(Lay::B_KVEMPTY + slot));
+            if (u == units - 1) tc_commit(bar(Lay::B_OFULL));
+          }
+          __syncwarp();
+          if (u + 2 < units) issue_s(u + 2);
+        }
+        n_ld += 2u * nj;
+        nq += it.two ? 2 : 1;
+      }
+      // Every product issued by this warp completes before TMEM is freed.
+      if (elect_one()) tc_commit(bar(Lay::B_DRAIN));
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, drain_wait(bar(Lay::B_DRAIN), 0u, kDrainLimitNs)) && lane == 0 && p.err)
+        atomicCAS(p.err, 0, timeout_code(kSiteTDrain));
+    } else if (F8) {
+      // ------------------------------------------------- split queries (E4M3)
+      // Warps 10 and 11 take every other row: scale by a power of two that brings the row's
+      // largest value into [128, 256), hi = E4M3(x), lo = E4M3(x - hi).
+      int nq = 0;
+      bool ok = true;
+      float* qs = reinterpret_cast<float*>(smem + Lay::QS_OFF);
+      for (int x = x0; x < x1 && ok;) {
+        const Seg it = list.at(x, x1);
+        x += it.j1 - it.j0;
+        for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
+          const int slot = nq & 1;
+          if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
+          if (!ok) break;
+          const int rows = (it.two ? (k ? it.nt - p.tpt : p.tpt) : it.nt) * p.G;
+          const int64_t tok = it.q0 + it.tok0 + k * p.tpt;
+          uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
+          // A row is held by D / 8 lanes, 8 values each.
+          constexpr int L = D / 8, R = 32 / L;
+          for (int r0 = (warp - 10) * R; r0 < rows; r0 += 2 * R) {
+            const int r = r0 + lane / L, c = lane % L;
+            const bool live = r < rows;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (live) {
+              const int t = r / p.G, gg = r - t * p.G;
+              w = __ldg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
+            }
+            float v[8];
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = __uint_as_float(u[i] << 16);
+              v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+              top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
+            }
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
+            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            e = max(-100, min(e, 120));
+            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+            if (live && c == 0) qs[slot * kBM + r] = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              hi[i] = lo[i] = 0;
+#pragma unroll
+              for (int k2 = 0; k2 < 2; ++k2) {
+                const float a = v[4 * i + 2 * k2] * up, b = v[4 * i + 2 * k2 + 1] * up;
+                const float ha = upper4(a), hb = upper4(b);
+                hi[i] |= pack_e4m3x2(ha, hb) << (16 * k2);
+                lo[i] |= pack_e4m3x2(a - ha, b - hb) << (16 * k2);
+              }
+            }
+            if (live) {
+              // 16-byte units of a row are permuted as the copies' swizzle does.
+              const int unit = c >> 1;
+              const int at = Lay::ROWB == 128 ? r * 128 + ((unit ^ (r & 7)) << 4) : r * 64 + ((unit ^ ((r >> 1) & 3)) << 4);
+              *reinterpret_cast<uint2*>(base + at + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(base + Lay::TILE + at + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Lay::B_QFULL + slot));
+        }
+      }
+    }
+  }
+
+  // The item whose first tiles this CTA holds without its last ones.
+  if (threadIdx.x == 0) {
+    int4 hd = make_int4(-1, 0, 0, 0);
+    if (x1 > x0) {
+      const Seg it = list.at(x1 - 1, x1);
+      const int begin = x1 - 1 - it.j0;  // position of the item's first tile
+      if (begin >= x0 && begin + it.kvt > x1) {
+        int last = static_cast<int>((static_cast<int64_t>(begin + it.kvt - 1) * ctas) / total);
+        while (static_cast<int64_t>(last + 1) * total / ctas <= begin + it.kvt - 1) ++last;
+        while (static_cast<int64_t>(last) * total / ctas > begin + it.kvt - 1) --last;
+        hd = make_int4(it.q0 + it.tok0, it.h, it.nt, last);
+      }
+    }
+    p.head[cta] = hd;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the items that were split: CTA c's second slot holds the first part, the
+// first slots of CTAs c + 1 .. last the others, in the order of the keys.  A warp per row.
+template <int D>
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int4 hd = p.head[c];
+  if (hd.x < 0) return;
+  const int i = blockIdx.y * 4 + (threadIdx.x >> 5);  // token i / G, head i % G
+  if (i >= hd.z * p.G) return;
+  const int t = i / p.G, g = i - t * p.G;
+  const int tile = t / p.tpt;
+  const int r = tile * kBM + (t - tile * p.tpt) * p.G + g;
+  const int parts = hd.w - c + 1;
+  auto at = [&](int k) -> int64_t { return (static_cast<int64_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * (2 * kBM) + r; };
+  float m = -INFINITY;
+  for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.stat[at(k)].x);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  constexpr int E = D / 32;
+  float acc[E] = {}, l = 0.f;
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    float w = 0.f, lk = 0.f;
+    if (k0 + lane < parts) {
+      const float2 st = p.stat[at(k0 + lane)];
+      w = st.x == -INFINITY ? 0.f : fast_exp2(st.x - m);
+      lk = st.y;
+    }
+    const int n = min(32, parts - k0);
+    for (int k = 0; k < n; k += 4) {
+      float v[4][E];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* src = p.part + at(k0 + min(k + q, n - 1)) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[q][0] = f.x; v[q][1] = f.y; v[q][2] = f.z; v[q][3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[q][0] = f.x; v[q][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float wk = __shfl_sync(0xffffffffu, w, (k + q) & 31), lq = __shfl_sync(0xffffffffu, lk, (k + q) & 31);
+        if (k + q < n && wk != 0.f) {
+          l = fmaf(wk, lq, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[q][e], acc[e]);
+        }
+      }
+    }
+  }
+  const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
+  const int64_t row = static_cast<int64_t>(hd.x + t) * p.Hq + hd.y * p.G + g;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if (lane == 0)
+    p.lse[static_cast<int64_t>(hd.y * p.G + g) * p.T + hd.x + t] = l > 0.f ? (m + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
+}
+
+constexpr int kMaxGrid = 160;  // CTAs the workspace has room for (148 SMs)
+
+template <int D, bool F8>
+cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
+                     int rows, cudaStream_t st) {
+  using Lay = Layout<D, F8>;
+  auto kern = tree_kernel<D, F8>;
+  const int smem = 1024 + Lay::TABLE_OFF + (4 * p.B + 2) * 4;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (rows + 3) / 4, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p);
 }
 
 }  // namespace
 
-size_t tree_workspace(int) { return 0; }
+// Parts, statistics and heads, each 256-byte aligned.
+size_t tree_workspace(int d) {
+  return static_cast<size_t>(kMaxGrid) * 2 * 256 * (d * sizeof(float) + sizeof(float2)) + kMaxGrid * 64;
+}
 
-cudaError_t launch_tree(const TreeArgs& a, int, cudaStream_t st) {
-  const int64_t warps = static_cast<int64_t>(a.T) * a.Hq;
-  const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
-  if (a.cache.d == 128) {
-    if (a.cache.e4m3) tree_kernel<128, true><<<grid, 128, 0, st>>>(a);
-    else tree_kernel<128, false><<<grid, 128, 0, st>>>(a);
-  } else {
-    if (a.cache.e4m3) tree_kernel<64, true><<<grid, 128, 0, st>>>(a);
-    else tree_kernel<64, false><<<grid, 128, 0, st>>>(a);
+attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError_t* cuda) {
+  const attn_cache_t& c = a.cache;
+  *cuda = cudaSuccess;
+  TreeParams p = {};
+  p.o = static_cast<__nv_bfloat16*>(a.o);
+  p.lse = a.lse;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.cu = a.cu;
+  p.slots = a.slots;
+  p.page_table = c.page_table;
+  p.lens = c.lens;
+  p.mask = a.mask;
+  p.mask_width = a.mask_width;
+  p.Hq = a.Hq;
+  p.heads = c.heads;
+  p.G = a.Hq / c.heads;
+  p.B = a.B;
+  p.T = a.T;
+  p.nslots = c.slots;
+  p.max_pages = c.max_pages;
+  p.pages = c.pages;
+  while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
+  p.layer_row = a.layer * c.pages * c.page_size;
+  p.rows = c.layers * c.pages * c.page_size;
+  p.box_rows = c.page_size < kBN ? c.page_size : kBN;
+  p.tpt = kBM / p.G;
+  const bool f8 = c.e4m3 != 0;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
+  p.o_scale = f8 ? c.v_scale : 1.f;
+  // P~ <= 2^tau; on the E4M3 path it carries 2^p_shift, so that at most 256 of E4M3's 448 is
+  // reached and small weights stay normal numbers.  A low tau leaves room for the shift; its
+  // rescales are rare once the maximum has settled.
+  p.tau = f8 ? 2.f : 8.f;
+  p.p_shift = f8 ? 6.f : 0.f;
+  p.err = a.err;
+  char* ws = static_cast<char*>(a.ws);
+  p.part = reinterpret_cast<float*>(ws);
+  ws += static_cast<size_t>(kMaxGrid) * 2 * 256 * c.d * sizeof(float);
+  p.stat = reinterpret_cast<float2*>(ws);
+  ws += static_cast<size_t>(kMaxGrid) * 2 * 256 * sizeof(float2);
+  p.head = reinterpret_cast<int4*>(ws);
+  // At most one item more per sequence than full row pairs, and no more tiles than the tables
+  // describe.
+  const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
+  const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
+  if (items > INT32_MAX / tiles) return ATTN_ERR_UNSUPPORTED;
+  int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
+  if (grid > kMaxGrid) grid = kMaxGrid;
+  const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
+  // {d, heads, rows} of K and V, one box per page (or 128 rows of it); q as {d, G, heads, T}.
+  const int esz = f8 ? 1 : 2, elems = (c.d * esz < 128 ? c.d : 128 / esz);
+  CUtensorMap tq = {}, tk, tv;
+  const uint64_t kvd[3] = {static_cast<uint64_t>(c.d), static_cast<uint64_t>(c.heads),
+                           static_cast<uint64_t>(c.layers) * c.pages * c.page_size};
+  const uint64_t kvs[2] = {static_cast<uint64_t>(c.d) * esz, static_cast<uint64_t>(c.heads) * c.d * esz};
+  const uint32_t kvb[3] = {static_cast<uint32_t>(elems), 1, static_cast<uint32_t>(p.box_rows)};
+  const int swizzle = elems * esz;
+  bool ok = attn_internal::make_tensor_map(&tk, c.k, esz, 3, kvd, kvs, kvb, swizzle) &&
+            attn_internal::make_tensor_map(&tv, c.v, esz, 3, kvd, kvs, kvb, swizzle);
+  if (ok && !f8) {
+    const uint64_t qd[4] = {static_cast<uint64_t>(c.d), static_cast<uint64_t>(p.G), static_cast<uint64_t>(c.heads),
+                            static_cast<uint64_t>(a.T)};
+    const uint64_t qs[3] = {static_cast<uint64_t>(c.d) * 2, static_cast<uint64_t>(p.G) * c.d * 2,
+                            static_cast<uint64_t>(a.Hq) * c.d * 2};
+    const uint32_t qb[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt)};
+    ok = attn_internal::make_tensor_map(&tq, a.q, 2, 4, qd, qs, qb, 128);
   }
-  return cudaGetLastError();
+  if (!ok) return ATTN_ERR_CUDA;
+  if (c.d == 128) *cuda = f8 ? launch_t<128, true>(tq, tk, tv, p, grid, rows, st) : launch_t<128, false>(tq, tk, tv, p, grid, rows, st);
+  else *cuda = f8 ? launch_t<64, true>(tq, tk, tv, p, grid, rows, st) : launch_t<64, false>(tq, tk, tv, p, grid, rows, st);
+  return ATTN_OK;
 }
 
 }  // namespace attn

@@ -292,7 +292,11 @@ attn_status_t attn_tree_fwd(const attn_cache_t* cache, int layer, const void* q,
   a.ws = workspace;
   int sms = 0;
   ATTN_TRY(device(&a.err, &sms));
-  return launched(attn::launch_tree(a, sms, cu(stream)), "attention kernel launch");
+  cudaError_t e = cudaSuccess;
+  const attn_status_t st = attn::launch_tree(a, sms, cu(stream), &e);
+  if (st == ATTN_ERR_UNSUPPORTED) return fail(st, "problem too large for 32-bit tile indexing");
+  if (st != ATTN_OK) return fail(st, "cuTensorMapEncodeTiled rejected the q/k/v views");
+  return launched(e, "attention kernel launch");
 }
 
 }  // extern "C"

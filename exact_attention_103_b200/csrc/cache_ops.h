@@ -65,6 +65,8 @@ struct TreeArgs {
   int* err;
 };
 size_t tree_workspace(int d);
-cudaError_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st);
+// ATTN_ERR_UNSUPPORTED: too many tiles for 32-bit counting; ATTN_ERR_CUDA: a tensor map was
+// rejected; otherwise *cuda is the launches' result.
+attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError_t* cuda);
 
 }  // namespace attn

@@ -157,7 +157,8 @@ ATTN_API attn_status_t attn_rope_append(const attn_cache_t* cache, int layer,
  * n_b <= mask_width <= 256), or j <= t when mask is NULL.  A token that sees nothing gets
  * O = 0 and LSE = -inf.  n_b = 0 is fine; rows outside [cu_q[0], cu_q[B]) are left alone.
  * What pages hold behind a sequence's end never counts; a key that no token of its sequence
- * sees may hold anything, but values of a sequence's own tokens must be finite.
+ * sees may hold anything, but values of a sequence's own tokens must be finite.  A cu_q
+ * that decreases or leaves [0, T] makes the whole call do nothing (error recorded).
  * An E4M3 cache is read as it is; queries and probabilities keep bf16's precision (each
  * is the sum of two E4M3 terms).
  * workspace: attn_tree_workspace_size(...) bytes, 256-byte aligned; calls that run at the
