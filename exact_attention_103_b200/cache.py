@@ -48,7 +48,9 @@ class CacheView(ctypes.Structure):
                 ("e4m3", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
-_TwoRows = Rows * 2
+_TwoRows, _ThreeRows = Rows * 2, Rows * 3
+_ROW = ctypes.sizeof(Rows)
+_at = ctypes.byref
 
 
 def declare(lib) -> None:
@@ -72,10 +74,14 @@ def declare(lib) -> None:
     lib.attn_tree_workspace_size.restype = cs
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+
+
 def _stream(dev: torch.device, stream: Optional[torch.cuda.Stream], *made) -> int:
     """The raw stream of a call; tensors this call made are kept until it has run there."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
+        return _current_stream(dev.index)
     for t in made:
         if t is not None:
             t.record_stream(stream)
@@ -84,7 +90,7 @@ def _stream(dev: torch.device, stream: Optional[torch.cuda.Stream], *made) -> in
 
 def _on(dev: torch.device, f, *args) -> None:
     """Calls the library with `dev` current; raises on an error status."""
-    if torch._C._cuda_getDevice() == dev.index:
+    if _current_device() == dev.index:
         st = f(*args)
     else:
         with torch.cuda.device(dev):
@@ -95,7 +101,7 @@ def _on(dev: torch.device, f, *args) -> None:
 
 def _list(t, name: str, dev: torch.device, n: Optional[int] = None) -> int:
     """The address of a contiguous int32 list on `dev`."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
         raise ValueError(f"{name} must be an int32 tensor")
     if t.device != dev:
         raise ValueError(f"{name} must be on {dev}")
@@ -109,6 +115,23 @@ def _list(t, name: str, dev: torch.device, n: Optional[int] = None) -> int:
 def _cuda(t, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
+    """The six strides of a tensor's rows and of its result's (y None: it has none), checked:
+    [*lead, H, d] with contiguous heads."""
+    if y is None:
+        y = x
+    for t, what in ((x, name), (y, "out of " + name)):
+        if t.dtype is not dtype or t.device != dev:
+            raise ValueError(f"{what} must be {dtype} on {dev}")
+    if y is not x and y.shape != shape:
+        raise ValueError(f"out of {name} has the wrong shape")
+    sx = x.stride()
+    sy = sx if y is x else y.stride()
+    if (sx[-1] != 1 or sy[-1] != 1) and x.numel():
+        raise ValueError(f"the values of a head of {name} must be contiguous")
+    return (sx[0] if batch else 0, sx[-3], sx[-2], sy[0] if batch else 0, sy[-3], sy[-2])
 
 
 class Rope:
@@ -167,55 +190,53 @@ class Rope:
         self.turns = torch.tensor([round(f / (2 * math.pi) * 2.0 ** 64) for f in freqs],
                                   dtype=torch.int64).to(device)
         self._view = RopePlan(self.turns.data_ptr(), dim, int(self.interleaved), self.amplitude)
+        self._ref = ctypes.byref(self._view)
 
 
 def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
     lib = _lib_of()
     _cuda(q, "q")
-    dev, dtype = q.device, q.dtype
-    if dtype not in _TYPES:
+    dev, dtype, shape = q.device, q.dtype, q.shape
+    kind = _TYPES.get(dtype)
+    if kind is None:
         raise ValueError("q must be bfloat16, float16 or float32")
     if plan.turns.device != dev:
         raise ValueError(f"the plan must be on {dev}")
     packed = cu_seqlens is not None
-    lead = q.shape[:-2]
-    if q.dim() != (3 if packed else 4):
+    if len(shape) != (3 if packed else 4):
         raise ValueError("packed q must be [T, H, d]" if packed else "dense q must be [B, N, H, d]")
-    if out is None:
-        out = (torch.empty(q.shape, dtype=dtype, device=dev),
-               None if k is None else torch.empty(k.shape, dtype=dtype, device=dev))
-        made = out
-    else:
-        made = ()
-        if k is None and isinstance(out, torch.Tensor):
-            out = (out, None)
-    rows = _TwoRows()
-    for i, (x, y, name) in enumerate(((q, out[0], "q"), (k, out[1], "k"))):
-        if x is None:
-            continue
-        _cuda(x, name)
-        _cuda(y, f"out of {name}")
-        if x.dtype != dtype or y.dtype != dtype or x.device != dev or y.device != dev:
-            raise ValueError("q, k and out must share a type and a device")
-        if x.shape[:-2] != lead or x.dim() != q.dim() or x.shape[-1] != q.shape[-1]:
+    if k is not None:
+        _cuda(k, "k")
+        k_shape = k.shape
+        if len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
             raise ValueError("q and k must hold the same tokens and head dim")
-        if y.shape != x.shape:
-            raise ValueError(f"out of {name} has the wrong shape")
-        sx, sy = x.stride(), y.stride()
-        if x.numel() and (sx[-1] != 1 or sy[-1] != 1):
-            raise ValueError(f"the values of a head of {name} must be contiguous")
-        r = rows[i]
-        r.src, r.dst, r.heads = x.data_ptr(), y.data_ptr(), x.shape[-2]
-        r.src_token, r.src_head, r.dst_token, r.dst_head = sx[-3], sx[-2], sy[-3], sy[-2]
-        if not packed:
-            r.src_batch, r.dst_batch = sx[0], sy[0]
-    B, N = (cu_seqlens.numel() - 1, lead[0]) if packed else lead
-    tokens = lead[0] if packed else B * N
+    made = ()
+    if out is None:
+        q_out, k_out = made = (torch.empty_like(q, memory_format=torch.contiguous_format),
+                               None if k is None else
+                               torch.empty_like(k, memory_format=torch.contiguous_format))
+    else:
+        q_out, k_out = (out, None) if isinstance(out, torch.Tensor) else out
+        _cuda(q_out, "out of q")
+        if k is not None:
+            _cuda(k_out, "out of k")
+    rows = _TwoRows()
+    rows[0] = (q.data_ptr(), q_out.data_ptr(), shape[-2],
+               *_rows(q, q_out, "q", dtype, dev, shape, not packed))
+    if k is not None:
+        rows[1] = (k.data_ptr(), k_out.data_ptr(), k_shape[-2],
+                   *_rows(k, k_out, "k", dtype, dev, k_shape, not packed))
+    if packed:
+        cu = _list(cu_seqlens, "cu_seqlens", dev)
+        B, tokens = cu_seqlens.numel() - 1, shape[0]
+        N = tokens
+    else:
+        cu, B, N = None, shape[0], shape[1]
+        tokens = B * N
     pos = None if positions is None else _list(positions, "positions", dev, tokens)
-    cu = None if cu_seqlens is None else _list(cu_seqlens, "cu_seqlens", dev)
-    _on(dev, lib.attn_rope, ctypes.byref(plan._view), inverse, _TYPES[dtype], rows,
-        1 if k is None else 2, q.shape[-1], B, N, cu, pos, _stream(dev, stream, *made))
-    return out[0] if k is None else (out[0], out[1])
+    _on(dev, lib.attn_rope, plan._ref, inverse, kind, rows, 1 if k is None else 2, shape[-1], B, N,
+        cu, pos, _stream(dev, stream, *made))
+    return q_out if k is None else (q_out, k_out)
 
 
 def rope_fwd(plan: Rope, q: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -289,6 +310,7 @@ class KVCache:
                                layers, pages, page_size, heads, d, slots, max_pages, int(e4m3),
                                self.k_scale, self.v_scale)
         self._ref = ctypes.byref(self._view)
+        self._ws = max(_lib_of().attn_tree_workspace_size(d), 256)
 
     @classmethod
     def empty(cls, layers: int, pages: int, page_size: int, heads: int, d: int, slots: int,
@@ -378,41 +400,36 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
     ``positions`` (int32 ``[T]``; default: the token's place in the cache).  Returns the rotated q
     (``out``; q itself is allowed), or None without q."""
     lib = _lib_of()
-    dev = cache.device
-    rows = []
-    if q is not None and out is None:
+    dev, bf16 = cache.device, torch.bfloat16
+    _cuda(k, "k")
+    _cuda(v, "v")
+    T, _, d = shape = k.shape if k.dim() == 3 else (0, 0, 0)
+    if d != cache.d or v.shape != shape:
+        raise ValueError(f"k and v must be [T, heads, {cache.d}]")
+    rows, made = _ThreeRows(), None
+    rows[1] = (k.data_ptr(), None, shape[1], *_rows(k, None, "k", bf16, dev, shape, False))
+    rows[2] = (v.data_ptr(), None, shape[1], *_rows(v, None, "v", bf16, dev, shape, False))
+    if q is not None:
         _cuda(q, "q")
-        out, made = torch.empty(q.shape, dtype=q.dtype, device=dev), True
-    else:
-        made = False
-    for x, y, name in ((q, out, "q"), (k, None, "k"), (v, None, "v")):
-        if x is None:
-            rows.append(None)
-            continue
-        _cuda(x, name)
-        if x.dtype != torch.bfloat16 or x.device != dev:
-            raise ValueError(f"{name} must be bfloat16 on {dev}")
-        if x.dim() != 3 or x.shape[0] != k.shape[0] or x.shape[2] != cache.d:
-            raise ValueError(f"{name} must be [T, H, {cache.d}]")
-        sx = x.stride()
-        if x.numel() and sx[2] != 1:
-            raise ValueError(f"the values of a head of {name} must be contiguous")
-        r = Rows(x.data_ptr(), None, x.shape[1], 0, sx[0], sx[1], 0, 0, 0)
-        if y is not None:
-            _cuda(y, "out")
-            if y.shape != x.shape or y.dtype != x.dtype or y.device != dev or (y.numel() and y.stride(2) != 1):
-                raise ValueError("out must be like q")
-            r.dst, r.dst_token, r.dst_head = y.data_ptr(), y.stride(0), y.stride(1)
-        rows.append(ctypes.byref(r))
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
+            raise ValueError(f"q must be [T, Hq, {cache.d}]")
+        if out is None:
+            out = made = torch.empty_like(q, memory_format=torch.contiguous_format)
+        else:
+            _cuda(out, "out")
+        rows[0] = (q.data_ptr(), out.data_ptr(), q_shape[1],
+                   *_rows(q, out, "q", bf16, dev, q_shape, False))
     if plan is not None and plan.turns.device != dev:
         raise ValueError(f"the plan must be on {dev}")
-    T, B = k.shape[0], cu_q.numel() - 1
-    _on(dev, lib.attn_rope_append, cache._ref, layer,
-        None if plan is None else ctypes.byref(plan._view), rows[0], rows[1], rows[2], B, T,
-        _list(cu_q, "cu_q", dev), None if slots is None else _list(slots, "slots", dev, B),
+    cu = _list(cu_q, "cu_q", dev)
+    B = cu_q.numel() - 1
+    _on(dev, lib.attn_rope_append, cache._ref, layer, None if plan is None else plan._ref,
+        None if q is None else _at(rows, 0), _at(rows, _ROW), _at(rows, 2 * _ROW), B, T, cu,
+        None if slots is None else _list(slots, "slots", dev, B),
         None if positions is None else _list(positions, "positions", dev, T),
-        _stream(dev, stream, out if made else None))
-    return out if q is not None else None
+        _stream(dev, stream, made))
+    return None if q is None else out
 
 
 def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
@@ -430,23 +447,25 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
     without a mask.  Returns (O ``[T, Hq, d]`` bf16, LSE ``[Hq, T]`` fp32, natural log); a token
     that sees nothing gets 0 and -inf.  The workspace is allocated with torch."""
     lib = _lib_of()
-    dev = cache.device
+    dev, d = cache.device, cache.d
     _cuda(q, "q")
-    if q.dtype != torch.bfloat16 or q.device != dev or not q.is_contiguous():
+    if q.dtype is not torch.bfloat16 or q.device != dev or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bfloat16 tensor on {dev}")
-    if q.dim() != 3 or q.shape[2] != cache.d:
-        raise ValueError(f"q must be [T, Hq, {cache.d}]")
-    T, Hq, d = q.shape
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d:
+        raise ValueError(f"q must be [T, Hq, {d}]")
+    T, Hq, _ = shape
+    cu = _list(cu_q, "cu_q", dev)
     B = cu_q.numel() - 1
-    made_o, made_l = out is None, lse is None
-    if made_o:
-        out = torch.empty_like(q)
-    elif not (out.is_cuda and out.device == dev and out.dtype == torch.bfloat16
-              and out.shape == q.shape and out.is_contiguous()):
+    made_o = made_l = None
+    if out is None:
+        out = made_o = torch.empty_like(q)
+    elif not (out.is_cuda and out.device == dev and out.dtype is torch.bfloat16
+              and out.shape == shape and out.is_contiguous()):
         raise ValueError("out must be like q")
-    if made_l:
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-    elif not (lse.is_cuda and lse.device == dev and lse.dtype == torch.float32
+    if lse is None:
+        lse = made_l = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    elif not (lse.is_cuda and lse.device == dev and lse.dtype is torch.float32
               and tuple(lse.shape) == (Hq, T) and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [Hq, T]")
     m, width = None, 0
@@ -457,11 +476,9 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
         if mask.dim() != 2 or mask.shape[0] != T or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous [T, width]")
         m, width = mask.data_ptr(), mask.shape[1]
-    bytes_ = lib.attn_tree_workspace_size(d)
-    ws = torch.empty(max(bytes_, 256), dtype=torch.uint8, device=dev)
+    ws = torch.empty(cache._ws, dtype=torch.uint8, device=dev)
     _on(dev, lib.attn_tree_fwd, cache._ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
-        Hq, B, T, _list(cu_q, "cu_q", dev),
-        None if slots is None else _list(slots, "slots", dev, B), m, width,
-        1.0 / math.sqrt(d) if scale is None else float(scale), ws.data_ptr(), ws.numel(),
-        _stream(dev, stream, ws, out if made_o else None, lse if made_l else None))
+        Hq, B, T, cu, None if slots is None else _list(slots, "slots", dev, B), m, width,
+        1.0 / math.sqrt(d) if scale is None else float(scale), ws.data_ptr(), cache._ws,
+        _stream(dev, stream, ws, made_o, made_l))
     return out, lse

@@ -29,11 +29,13 @@
 // significant bits, the second 4 more).  Each costs one more product, at twice bf16's rate.
 //
 // Warp roles (384 threads): 0-3 and 4-7 softmax, correction and epilogue of streams 0 and 1;
-// 8 TMA producer; 9 TMEM owner and tcgen05.mma issuer; 10 and 11 write the split queries of
-// E4M3 caches (idle otherwise).  Every wait is bounded; on expiry the CTA stops, drains its
+// 8 and 10 TMA producers of K (and q) and of V; 9 (TMEM owner) and 11 issue S and P~V.  The softmax
+// warps write an E4M3 cache's split queries.  Every wait is bounded; on expiry the CTA stops, drains its
 // copies and products, frees TMEM and returns.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+
+#include <atomic>
 
 #include "attn_internal.h"
 #include "cache_ops.h"
@@ -50,7 +52,7 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 enum TreeSite : int {  // wait sites of the device error word (16..30)
   kSiteTQFull = 16, kSiteTQEmpty, kSiteTKvFull, kSiteTKvEmpty, kSiteTSFull, kSiteTPFull, kSiteTOFull, kSiteTMerge,
-  kSiteTDrain
+  kSiteTDrain, kSiteTPvDone
 };
 __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
 
@@ -68,13 +70,14 @@ struct TreeParams {
   int box_rows;    // rows of one K/V copy: min(page size, 128)
   int tpt;         // tokens of a 128-row tile: 128 / G
   float scale_log2, o_scale, tau, p_shift;
-  float* part;     // [grid][2][256][D] unnormalised O
+  float* part;     // [grid][2][D / 4][256][4] unnormalised O: four columns of neighbouring rows
+                   // lie together, as the lanes that write and join them are neighbouring rows
   float2* stat;    // [grid][2][256] (maximum in log2 units, sum)
   int4* head;      // [grid] the item whose first tiles this CTA left unfinished
   int* err;
 };
 
-// head[c]: x = global row of its first token (-1: none), y = cache head, z = tokens, w = last CTA.
+// head[c]: x = row of q of its first token (-1: none), y = cache head, z = tokens, w = last CTA.
 
 template <int D, bool F8>
 struct Layout {
@@ -92,29 +95,37 @@ struct Layout {
   static constexpr int ML_OFF = KV_OFF + NSTAGE * TILE;      // float2 [2][128]: (m, l) of the two streams
   static constexpr int QS_OFF = ML_OFF + 2 * kBM * 8;        // float [2][128]: 1 / scale of the split queries
   static constexpr int BAR_OFF = QS_OFF + 2 * kBM * 4;
-  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 6, B_OFULL = 10, B_ML = 11, B_EPI = 12,
-                       B_DRAIN = 13, B_KVFULL = 14, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
+  // SFULL, PFULL, PVDONE: one per S buffer; DRAIN: one per issuing warp
+  static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 8, B_PVDONE = 12, B_OFULL = 16, B_ML = 17,
+                       B_EPI = 18, B_DRAIN = 19, B_KVFULL = 21, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int TABLE_OFF = MISC_OFF + 128;
-  static constexpr int TM_S0 = 0, TM_S1 = 128, TM_O0 = 256, TM_O1 = 256 + D;
+  // Cost of a key tile with one and with two row tiles: the copies bound the first, the softmax
+  // of 256 rows the second.
+  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 1, COST_PAIR = ESZ * D == 256 ? 4 : 2;
+  static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 256 + D;  // S: four buffers of 64 columns
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// One CTA's stretch of an item: key tiles [j0, j1) of kvt.
+// One CTA's stretch of an item: key tiles [j0, j1) of kvt (none if j0 >= j1).
 struct Seg {
   int h, tok0, nt;        // cache head; first token (of the sequence) and number of tokens
   int n, ctx, len, slot;  // the sequence: drafted tokens, context, tokens in the cache, slot
   int q0;                 // its first row of q
   int j0, j1, kvt;
+  int begin, next;        // where the item begins in the list, and the next stretch
   bool two;               // more than one row tile
 };
 
-// The list of work, decoded alike by every role.  Tables in shared memory, per sequence:
-// cum (tiles before it), first row of q, slot, tokens in the cache.
+// The list of work, decoded alike by every role: items (sequence, cache head, row pair) one
+// behind the other, each key tile as long as its cost (`one` or `two` row tiles).  A tile
+// belongs to the CTA whose part holds its first unit; parts are no shorter than the longest
+// tile, so a part inside an item holds one of its tiles.  Tables in shared memory, per
+// sequence: cum (cost before it), first row of q, slot, tokens in the cache.
 struct List {
   const int *cum, *cu, *slot, *len;
-  int B, heads, tpt;
+  int B, heads, tpt, one, pair;
   bool masked;
 
   // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
@@ -123,6 +134,7 @@ struct List {
     const int end = masked ? n : min((rt + 1) * 2 * tpt, n);
     return (length - n + end + kBN - 1) / kBN;
   }
+  __device__ __forceinline__ int cost(int n, int rt) const { return n - rt * 2 * tpt > tpt ? pair : one; }
   __device__ __forceinline__ Seg at(int x, int end) const {
     int lo = 0, hi = B - 1;  // the sequence with cum[b] <= x < cum[b + 1]
     while (lo < hi) {
@@ -139,24 +151,49 @@ struct List {
     int r = x - cum[lo];
     s.h = r / per_head;
     r -= s.h * per_head;
-    int rt = 0, kv = tiles(s.n, s.len, 0);
-    while (r >= kv) {
-      r -= kv;
-      kv = tiles(s.n, s.len, ++rt);
+    int rt = 0, kv = tiles(s.n, s.len, 0), w = cost(s.n, 0);
+    while (r >= kv * w) {
+      r -= kv * w;
+      ++rt;
+      kv = tiles(s.n, s.len, rt);
+      w = cost(s.n, rt);
     }
     s.tok0 = rt * 2 * tpt;
     s.nt = min(2 * tpt, s.n - s.tok0);
     s.two = s.nt > tpt;
     s.kvt = kv;
-    s.j0 = r;
-    s.j1 = min(kv, r + end - x);
+    s.begin = x - r;
+    s.next = min(end, s.begin + kv * w);
+    s.j0 = ceil_div(r, w);
+    s.j1 = ceil_div(s.next - s.begin, w);
     return s;
   }
 };
 
-// The order of K and V tiles in the ring.  The products run as units: S(u) and P~V(u), with
-// S two units ahead.  One row tile: unit u is key tile u, so K runs two tiles ahead of V; two
-// row tiles: units 2j and 2j + 1 are key tile j, K runs one ahead.
+// The products run as units of 64 keys, S(u) four units ahead of P~V(u); unit u belongs to stream
+// u % 2, and its S (then P~) lies in buffer u % 4, so that a stream finds its next S computed
+// while it works on one.  Two row tiles: the streams take the same half tiles; one: stream s
+// takes tiles j0 + s, j0 + s + 2, ...  A second half that lies behind the sequence's end is
+// left out.
+struct Unit {
+  int j, half;  // tile (from j0) and half
+  bool live;
+};
+__device__ __forceinline__ Unit unit_at(const Seg& it, int u) {
+  const int v = u >> 1, s = u & 1, nj = it.j1 - it.j0;
+  Unit x;
+  x.half = v & 1;
+  x.j = it.two ? v >> 1 : 2 * (v >> 1) + s;
+  x.live = x.j < nj && (x.half == 0 || it.len - (it.j0 + x.j) * kBN > kBN / 2);
+  return x;
+}
+__device__ __forceinline__ int unit_count(const Seg& it) {
+  const int nj = it.j1 - it.j0;
+  return 4 * (it.two ? nj : (nj + 1) / 2);
+}
+
+// The order of K and V tiles in the ring: K runs `lead` tiles ahead of V (two row tiles: 1,
+// one: 2, a tile of each stream).
 __device__ __forceinline__ int k_pos(int j, int lead) { return j + max(0, j - lead + 1); }
 __device__ __forceinline__ int v_pos(int j, int n, int lead) { return j + min(n, j + lead); }
 
@@ -201,15 +238,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(bar(Lay::B_QFULL + s), F8 ? 2 : 1);
-      mbar_init(bar(Lay::B_QEMPTY + s), F8 ? 9 : 1);  // E4M3: and the softmax warps, with the row scales
-      mbar_init(bar(Lay::B_SFULL + s), 1);
-      for (int h = 0; h < 2; ++h) mbar_init(bar(Lay::B_PFULL + 2 * s + h), 4);
+      mbar_init(bar(Lay::B_QFULL + s), F8 ? 8 : 1);  // E4M3: written by the softmax warps
+      mbar_init(bar(Lay::B_QEMPTY + s), 1);
+      mbar_init(bar(Lay::B_DRAIN + s), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(Lay::B_SFULL + i), 1);
+      mbar_init(bar(Lay::B_PFULL + i), 4);
+      mbar_init(bar(Lay::B_PVDONE + i), 1);
     }
     mbar_init(bar(Lay::B_OFULL), 1);
     mbar_init(bar(Lay::B_ML), 8);
     mbar_init(bar(Lay::B_EPI), 8);
-    mbar_init(bar(Lay::B_DRAIN), 1);
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(Lay::B_KVFULL + i), 1);
       mbar_init(bar(Lay::B_KVEMPTY + i), 1);
@@ -229,6 +269,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   list.B = p.B;
   list.heads = p.heads;
   list.tpt = p.tpt;
+  list.one = Lay::COST_ONE;
+  list.pair = Lay::COST_PAIR;
   list.masked = p.mask != nullptr;
   {
     // The tiles of each sequence and their prefix sum; a thread takes consecutive sequences.
@@ -253,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) {
           record_invalid(p.err, bad);
         } else {
-          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.tiles(n, len, rt);
+          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.tiles(n, len, rt) * list.cost(n, rt);
           work *= p.heads;
         }
       }
@@ -290,7 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = misc[0];
   const int total = t_cum[p.B];
-  const int ctas = min(static_cast<int>(gridDim.x), total);  // CTAs with work: one tile at least
+  // CTAs with work; a part holds at least one tile
+  const int ctas = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / Lay::COST_PAIR)) : 0;
   const int cta = static_cast<int>(blockIdx.x);
   const int x0 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta) * total / ctas) : 0;
   const int x1 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta + 1) * total / ctas) : 0;
@@ -302,6 +345,76 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, wc, timeout_code(site)));
   };
 
+  // E4M3: softmax warp w writes its eighth of an item's queries, from q slot nq on: each row is
+  // scaled by the power of two that brings its largest value into [128, 256), hi = E4M3(x), lo =
+  // E4M3(x - hi).
+  auto split_q = [&](const Seg& it, int nq, int w8) -> bool {
+    float* qs = reinterpret_cast<float*>(smem + Lay::QS_OFF);
+    for (int k = 0; k < (it.two ? 2 : 1); ++k, ++nq) {
+      const int slot = nq & 1;
+      if (nq >= 2 && !wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty)) return false;
+      const int rows = (it.two ? (k ? it.nt - p.tpt : p.tpt) : it.nt) * p.G;
+      const int64_t tok = it.q0 + it.tok0 + k * p.tpt;
+      uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
+      // A row is held by D / 8 lanes, 8 values each; 4 steps are in flight together.
+      constexpr int L = D / 8, R = 32 / L, U = 4;
+      const int c = lane % L;
+      for (int r0 = w8 * R + lane / L; __any_sync(0xffffffffu, r0 < rows); r0 += 8 * R * U) {
+        uint4 w[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int r = r0 + 8 * R * i, t = r / p.G, gg = r - t * p.G;
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (r < rows) w[i] = __ldg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int r = r0 + 8 * R * i;
+          if (!__any_sync(0xffffffffu, r < rows)) break;
+          float v[8];
+          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          float top = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(u[e] << 16);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+          }
+#pragma unroll
+          for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          e = max(-100, min(e, 120));
+          const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            hi[y] = lo[y] = 0;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
+              const float ha = upper4(a), hb = upper4(b);
+              hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
+              lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
+            }
+          }
+          if (r < rows) {
+            if (c == 0) qs[slot * kBM + r] = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+            // 16-byte units of a row are permuted as the copies' swizzle does.
+            const int unit = c >> 1;
+            const int at = Lay::ROWB == 128 ? r * 128 + ((unit ^ (r & 7)) << 4) : r * 64 + ((unit ^ ((r >> 1) & 3)) << 4);
+            *reinterpret_cast<uint2*>(base + at + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(base + Lay::TILE + at + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Lay::B_QFULL + slot));
+    }
+    return true;
+  };
+
   // 4 x 32 x (168 - 120) registers released by warpgroup 2, 8 x 32 x (192 - 168) taken.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n" ::: "memory");
@@ -310,85 +423,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp >> 2, wq = warp & 3;
     const int r = wq * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t t_s = tmem + lane_bits + (s ? Lay::TM_S1 : Lay::TM_S0);
     const uint32_t t_o = tmem + lane_bits + (s ? Lay::TM_O1 : Lay::TM_O0);
     const int tl = r / p.G, g = r - tl * p.G;  // token of the tile, head of the group
     float2* ml = reinterpret_cast<float2*>(smem + Lay::ML_OFF);
-    uint32_t s_phase = 0, o_phase = 0, m_phase = 0, e_phase = 0;
+    uint32_t phases = 0;  // bit u & 3: phase of that buffer's next use
+    uint32_t o_phase = 0, m_phase = 0, e_phase = 0;
     int nq = 0;  // row tiles of q taken so far
     bool ok = true;
+    int4 hd = make_int4(-1, 0, 0, 0);  // the item whose first tiles this CTA holds without its last
     for (int x = x0; x < x1 && ok;) {
       const Seg it = list.at(x, x1);
-      x += it.j1 - it.j0;
+      x = it.next;
+      if (it.j0 >= it.j1) continue;
+      if (it.j0 == 0 && it.j1 < it.kvt) {
+        // the CTA whose part holds the first unit of the item's last tile
+        const int64_t end = it.begin + (it.kvt - 1) * (it.two ? list.pair : list.one);
+        int last = static_cast<int>(end * ctas / total);
+        while (static_cast<int64_t>(last + 1) * total / ctas <= end) ++last;
+        while (static_cast<int64_t>(last) * total / ctas > end) --last;
+        hd = make_int4(it.q0 + it.tok0, it.h, it.nt, last);
+      }
       const int first = it.two ? s * p.tpt : 0;  // this stream's first token of the item
       const int mine = it.two ? (s ? it.nt - p.tpt : p.tpt) : it.nt;
       const int tok = it.tok0 + first + tl;      // this row's token of the sequence
       const bool valid = tl < mine;
       const bool busy = wq * 32 < mine * p.G;    // the warp has a valid row
-      const int jstep = it.two ? 1 : 2;
       float sl = p.scale_log2;
       if constexpr (F8) {
+        ok = split_q(it, nq, warp);
+        if (!ok) break;
+        // every warp has written its rows' scales
         const int mine_q = nq + (it.two ? s : 0);
         ok = wait(Lay::B_QFULL + (mine_q & 1), (mine_q >> 1) & 1, kSiteTQFull);
         if (!ok) break;
         sl = p.scale_log2 * reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(Lay::B_QEMPTY + (nq & 1)));
-          if (it.two) mbar_arrive(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
-        }
       }
+      nq += it.two ? 2 : 1;
       float m_ref = -INFINITY, l = 0.f;
       bool any = false;
-      for (int j = it.j0 + (it.two ? 0 : s); j < it.j1; j += jstep) {
-        ok = wait(Lay::B_SFULL + s, s_phase, kSiteTSFull);
+      int last_buf = 0;  // buffer of the stream's last unit
+      const int units = unit_count(it);
+      for (int u = s; u < units; u += 2) {
+        const Unit un = unit_at(it, u);
+        if (!un.live) continue;
+        const int buf = u & 3;
+        const uint32_t t_s = tmem + lane_bits + Lay::TM_S + 64 * buf;
+        ok = wait(Lay::B_SFULL + buf, (phases >> buf) & 1u, kSiteTSFull);
         if (!ok) break;
-        s_phase ^= 1u;
+        phases ^= 1u << buf;
         tc_fence_after();
-        any = true;
-        auto release = [&](int half) {
+        auto release = [&]() {
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Lay::B_PFULL + 2 * s + half));
+          if (lane == 0) mbar_arrive(bar(Lay::B_PFULL + buf));
         };
+        const bool again = any;  // O holds something
+        any = true;
         if (!busy) {  // nothing to compute: the rows of P~ that stay behind are never read
-          release(0);
-          release(1);
+          release();
+          last_buf = buf;
           continue;
         }
-        uint32_t sa[64], sz[64];
+        uint32_t sa[64];
         tmem_ld_x64(t_s, sa);
-        tmem_ld_x64_async(t_s + 64, sz);
-        const int kb = j * kBN;
-        const bool part = kb + kBN > it.ctx;  // the tile holds drafted tokens, or ends behind them
-        uint32_t vis[4] = {~0u, ~0u, ~0u, ~0u};
-        if (part) {
+        const int kb = (it.j0 + un.j) * kBN + 64 * un.half;
+        if (kb + 64 > it.ctx) {  // the half tile holds drafted tokens, or ends behind them
+          uint32_t vis[2];
           if (p.mask == nullptr) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) vis[c] = below(it.ctx + tok + 1 - kb, c);
+            for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx + tok + 1 - kb, c);
           } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) vis[c] = below(it.ctx - kb, c);
-            // The mask rows of the warp's tokens, 32 columns per load, 4 tokens at a time.
+            for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx - kb, c);
+            // The mask rows of the warp's tokens, 32 columns per load, 8 tokens at a time.
             const int t_lo = (wq * 32) / p.G, t_hi = min((wq * 32 + 31) / p.G, mine - 1);
             const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first) * p.mask_width;
             const int col = kb + lane - it.ctx;
-            for (int t0 = t_lo; t0 <= t_hi; t0 += 4) {
-              uint8_t w[4][4];
+            for (int t0 = t_lo; t0 <= t_hi; t0 += 8) {
+              uint8_t w[8][2];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                   const int jl = col + 32 * c;
                   w[i][c] = (t0 + i <= t_hi && jl >= 0 && jl < it.n)
                                 ? __ldg(rows + static_cast<int64_t>(t0 + i) * p.mask_width + jl)
                                 : 0;
                 }
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int c = 0; c < 2; ++c) {
                   const uint32_t bits = __ballot_sync(0xffffffffu, w[i][c] != 0);
                   if (t0 + i == tl) vis[c] |= bits;
                 }
@@ -409,21 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             m4[i] = fmax3(m4[i], __uint_as_float(sa[c + i]), __uint_as_float(sa[c + 4 + i]));
 #pragma unroll
         for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(sa[60 + i]));
-        tmem_wait_ld_x64(sz);
-        if (part) {
-#pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((vis[2 + (c >> 5)] >> (c & 31)) & 1u)) sz[c] = __float_as_uint(-INFINITY);
-        }
-#pragma unroll
-        for (int c = 0; c < 64; c += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            m4[i] = fmax3(m4[i], __uint_as_float(sz[c + i]), __uint_as_float(sz[c + 4 + i]));
         const float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sl;
         bool need = false;
         float alpha = 1.f;
-        if (m_ref == -INFINITY) {  // the first tile with a key that this row sees
+        if (m_ref == -INFINITY) {  // the first keys that this row sees
           m_ref = m_tile;
         } else if (m_tile - m_ref > p.tau) {
           need = valid;
@@ -434,23 +549,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float nm = m_ref == -INFINITY ? 0.f : -m_ref;
         if constexpr (F8) nm += p.p_shift;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        auto rescale = [&]() {
-          // O of this stream is stable: the commit that signalled S also covers its last P~V.
-          if (__any_sync(0xffffffffu, need)) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t ov[32];
-              tmem_ld_x32(t_o + 32 * c, ov);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-              tmem_st_x32(t_o + 32 * c, ov);
-            }
-          }
-        };
         auto exps = [&](int c, float& a, float& e) {  // column pair c (keys 2c, 2c + 1)
-          const uint32_t y0 = c < 32 ? sa[2 * c] : sz[2 * c - 64];
-          const uint32_t y1 = c < 32 ? sa[2 * c + 1] : sz[2 * c - 63];
-          ffma2_bc(a, e, __uint_as_float(y0), __uint_as_float(y1), sl, nm);
+          ffma2_bc(a, e, __uint_as_float(sa[2 * c]), __uint_as_float(sa[2 * c + 1]), sl, nm);
           a = fast_exp2(a);
           e = fast_exp2(e);
           if (c & 1) fadd2_acc(ls[2], ls[3], a, e);
@@ -459,45 +559,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!F8) {
           uint32_t pk[32];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int cc = 0; cc < 32; ++cc) {
-              float a, e;
-              exps(32 * half + cc, a, e);
-              pk[cc] = pack_bf16x2(a, e);
-            }
-            tmem_st_x32(t_s + 32 * half, pk);
-            if (half == 0) rescale();
-            release(half);
+          for (int c = 0; c < 32; ++c) {
+            float a, e;
+            exps(c, a, e);
+            pk[c] = pack_bf16x2(a, e);
           }
+          tmem_st_x32(t_s, pk);
         } else {
           // P~ = hi + lo; the conversion of hi is exact while it is a normal E4M3 number.
           uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-#pragma unroll
-            for (int cc = 0; cc < 32; ++cc) {
-              float a, e;
-              exps(32 * half + cc, a, e);
-              const float ha = upper4(a), he = upper4(e);
-              const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(a - ha, e - he);
-              if (cc & 1) {
-                hi[cc >> 1] |= wh << 16;
-                lo[cc >> 1] |= wl << 16;
-              } else {
-                hi[cc >> 1] = wh;
-                lo[cc >> 1] = wl;
-              }
+          for (int c = 0; c < 32; ++c) {
+            float a, e;
+            exps(c, a, e);
+            const float ha = upper4(a), he = upper4(e);
+            const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(a - ha, e - he);
+            if (c & 1) {
+              hi[c >> 1] |= wh << 16;
+              lo[c >> 1] |= wl << 16;
+            } else {
+              hi[c >> 1] = wh;
+              lo[c >> 1] = wl;
             }
-            tmem_st_x16(t_s + 16 * half, hi);
-            tmem_st_x16(t_s + 32 + 16 * half, lo);
-            if (half == 0) rescale();
-            release(half);
+          }
+          tmem_st_x16(t_s, hi);
+          tmem_st_x16(t_s + 16, lo);
+        }
+        if (again && __any_sync(0xffffffffu, need)) {
+          // the stream's last P~V has to be in O before O is rescaled
+          ok = wait(Lay::B_PVDONE + last_buf, ((phases >> last_buf) & 1u) ^ 1u, kSiteTPvDone);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld_x32(t_o + 32 * c, ov);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st_x32(t_o + 32 * c, ov);
           }
         }
+        last_buf = buf;
+        release();
         l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
       }
-      nq += it.two ? 2 : 1;
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
       // Two row tiles: each warpgroup writes its own rows.  One: the streams' O are joined, and
@@ -524,11 +629,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = it.j0 == 0 && it.j1 == it.kvt;
       if (busy) {
         const int64_t row = static_cast<int64_t>(it.q0 + tok) * p.Hq + it.h * p.G + g;
-        const int64_t slot_row = (static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0)) * (2 * kBM) + (it.two ? s * kBM : 0) + r;
+        const int64_t slot = static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0);
+        const int slot_row = (it.two ? s * kBM : 0) + r;
+        float4* part = reinterpret_cast<float4*>(p.part) + slot * (2 * kBM) * (D / 4) + slot_row;
         const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
         // Columns of this warpgroup; a stream that took no tile has nothing in its O.
         const int c_lo = it.two ? 0 : s * (D / 64), c_hi = it.two ? D / 32 : (s + 1) * (D / 64);
-        const bool use_own = any, use_other = !it.two && (s ? true : it.j1 - it.j0 > 1);
+        const bool use_own = any, use_other = !it.two && (s != 0 || it.j1 - it.j0 > 1);
         const uint32_t t_x = tmem + lane_bits + (s ? Lay::TM_O0 : Lay::TM_O1);
         for (int c = c_lo; c < c_hi; ++c) {
           uint32_t ov[32];
@@ -558,9 +665,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
                                   pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
           } else if (valid) {
-            float4* dst = reinterpret_cast<float4*>(p.part + slot_row * D + 32 * c);
+            float4* dst = part + c * 8 * (2 * kBM);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              dst[i * (2 * kBM)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
           __syncwarp();
         }
@@ -569,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] =
                 l > 0.f ? (m_ref + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
           } else {
-            p.stat[slot_row] = make_float2(m_ref, l);
+            p.stat[slot * (2 * kBM) + slot_row] = make_float2(m_ref, l);
           }
         }
       }
@@ -581,26 +689,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(Lay::B_EPI, e_phase, kSiteTMerge);
       e_phase ^= 1u;
     }
+    if (threadIdx.x == 0) p.head[cta] = hd;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n" ::: "memory");
-    if (warp == 8) {
-      // ----------------------------------------------------------- producer
+    if (warp == 8 || warp == 10) {
+      // --------------------------------------------------- producers: K (and q), V
+      const bool is_k = warp == 8;
+      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
       if (elect_one()) {
-        tma_prefetch_map(&tm_q);
-        tma_prefetch_map(&tm_k);
-        tma_prefetch_map(&tm_v);
+        if (is_k && !F8) tma_prefetch_map(&tm_q);
+        tma_prefetch_map(map);
       }
       __syncwarp();
       const uint64_t pol = l2_policy_evict_normal();
       uint32_t n_ld = 0;
+      int mine = -1;  // lane i: this warp's last copy into ring slot i
       int nq = 0;
       bool ok = true;
       const int per_tile = kBN / p.box_rows;  // copies of a full tile
       for (int x = x0; x < x1 && ok;) {
         const Seg it = list.at(x, x1);
-        x += it.j1 - it.j0;
+        x = it.next;
+        if (it.j0 >= it.j1) continue;
+        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
+        // The pages of 32 copies, one per lane, and of the next 32.
+        const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
+        auto pages_from = [&](int box) -> int {
+          const int pos = it.j0 * kBN + (box + lane) * p.box_rows;
+          return (box < nj * per_tile && pos < it.len) ? __ldg(row + (pos >> p.page_shift)) : 0;
+        };
+        int win = pages_from(0), win_next = pages_from(32);
+        const int tiles_per_win = 32 / per_tile;
         if constexpr (!F8) {
           for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
+            if (!is_k) continue;
             const int slot = nq & 1;
             if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
             if (!ok) break;
@@ -615,27 +737,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
-        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
-        // Lane i's copy of a tile: rows box_rows * i ..; its page is looked up one tile ahead.
-        auto page_at = [&](int j) -> int {
-          const int pos = (it.j0 + j) * kBN + lane * p.box_rows;
-          return (j < nj && lane < per_tile && pos < it.len) ? __ldg(row + (pos >> p.page_shift)) : 0;
-        };
-        int next_k = page_at(0), next_v = next_k;
-        int kj = 0, vj = 0;
-        while (vj < nj && ok) {
-          const bool is_k = kj < nj && kj < vj + lead;
-          const int j = is_k ? kj : vj;
-          const int page = is_k ? next_k : next_v;
-          if (is_k) next_k = page_at(++kj);
-          else next_v = page_at(++vj);
-          const uint32_t slot = n_ld % NS;
-          if (n_ld >= static_cast<uint32_t>(NS))
-            ok = wait(Lay::B_KVEMPTY + slot, ((n_ld / NS) - 1) & 1u, kSiteTKvEmpty);
-          if (!ok) break;
+        for (int j = 0; j < nj; ++j) {
+          if (j > 0 && j % tiles_per_win == 0) {
+            win = win_next;
+            win_next = pages_from((j / tiles_per_win + 1) * 32);
+          }
+          const uint32_t n = n_ld + (is_k ? k_pos(j, lead) : v_pos(j, nj, lead)), slot = n % NS;
+          if (n >= static_cast<uint32_t>(NS)) {
+            ok = wait(Lay::B_KVEMPTY + slot, ((n / NS) - 1) & 1u, kSiteTKvEmpty);
+            if (!ok) break;
+          }
           const int kb = (it.j0 + j) * kBN;
           const int copies = min(per_tile, ceil_div(it.len - kb, p.box_rows));
+          const int page = __shfl_sync(0xffffffffu, win, (j % tiles_per_win) * per_tile + (lane & (per_tile - 1)));
+          if (lane == static_cast<int>(slot)) mine = static_cast<int>(n);
           if (lane == 0) mbar_arrive_expect_tx(bar(Lay::B_KVFULL + slot), copies * p.box_rows * Lay::ROWB * Lay::NCHUNK);
           __syncwarp();
           if (lane < copies) {
@@ -646,222 +761,160 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t dst = sb + Lay::KV_OFF + slot * Lay::TILE + lane * p.box_rows * Lay::ROWB;
 #pragma unroll
             for (int c = 0; c < Lay::NCHUNK; ++c)
-              tma_load_3d(dst + c * Lay::CHUNK, is_k ? &tm_k : &tm_v, bar(Lay::B_KVFULL + slot), c * Lay::CELEMS, it.h, at, pol);
+              tma_load_3d(dst + c * Lay::CHUNK, map, bar(Lay::B_KVFULL + slot), c * Lay::CELEMS, it.h, at, pol);
           }
           __syncwarp();
-          ++n_ld;
         }
+        n_ld += 2u * nj;
       }
-      // Every copy has landed before the CTA may exit.
-      const uint32_t first = n_ld > static_cast<uint32_t>(NS) ? n_ld - NS : 0u;
-      for (uint32_t n = first; n < n_ld; ++n) drain_wait(bar(Lay::B_KVFULL + n % NS), (n / NS) & 1u, kDrainLimitNs);
-      if constexpr (!F8) {
+      // This warp's copies have landed before the CTA may exit.  On an early end the other
+      // producer may have refilled a slot, which then runs out the limit.
+      for (int i = 0; i < NS; ++i) {
+        const int n = __shfl_sync(0xffffffffu, mine, i);
+        if (n >= 0 && (!ok || n + NS >= static_cast<int>(n_ld)))
+          drain_wait(bar(Lay::B_KVFULL + i), (n / NS) & 1, ok ? kDrainLimitNs : kDrainLimitNs / 8);
+      }
+      if (!F8 && is_k) {
         for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n) drain_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, kDrainLimitNs);
       }
-    } else if (warp == 9) {
-      // ---------------------------------------------------------------- MMA
-      constexpr uint32_t idesc_s = F8 ? idesc_e4m3_f32(kBM, kBN, 0, 0) : idesc_bf16_f32(kBM, kBN, 0, 0);
-      constexpr uint32_t idesc_o = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
+    } else {
+      // ------------------------------------------------- products: S (9), P~V (11)
+      // Two warps issue them, so that one's waits run beside the other's products: a lone
+      // issuer spent as long waiting as the products took.
+      constexpr int kHalf = kBN / 2;
       constexpr bool SW64 = Lay::ROWB == 64;
-      auto k_desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
-      uint32_t n_ld = 0, p_phase0 = 0, p_phase1 = 0;
+      uint32_t n_ld = 0, phases = 0, used = 0;  // bit b: phase of S buffer b, and whether it was used
       int nq = 0;
       bool ok = true;
       for (int x = x0; x < x1 && ok;) {
         const Seg it = list.at(x, x1);
-        x += it.j1 - it.j0;
-        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2, units = it.two ? 2 * nj : nj;
-        for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k)
-          ok = wait(Lay::B_QFULL + ((nq + k) & 1), ((nq + k) >> 1) & 1, kSiteTQFull);
-        if (!ok) break;
-        tc_fence_after();
-        auto issue_s = [&](int u) {
-          const int j = it.two ? u >> 1 : u, s = u & 1;
-          const uint32_t n = n_ld + k_pos(j, lead), slot = n % NS;
-          if (!it.two || s == 0) {
-            ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
-            if (!ok) return;
-            tc_fence_after();
-          }
-          const int qslot = (nq + (it.two ? s : 0)) & 1;
-          const uint32_t tS = tmem + (s ? Lay::TM_S1 : Lay::TM_S0);
-          const uint32_t qbase = sb + Lay::Q_OFF + qslot * Lay::QTILE, kbase = sb + Lay::KV_OFF + slot * Lay::TILE;
-          if (elect_one()) {
-            const uint64_t db0 = k_desc(kbase);
-#pragma unroll
-            for (int term = 0; term < (F8 ? 2 : 1); ++term) {
-              const uint64_t da0 = k_desc(qbase + term * Lay::TILE);
-              constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
-#pragma unroll
-              for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
-                const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
-                const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
-                if constexpr (F8) mma_ss_f8(tS, desc_add(da0, off), desc_add(db0, off), idesc_s, acc);
-                else mma_ss(tS, desc_add(da0, off), desc_add(db0, off), idesc_s, acc);
-              }
-            }
-            tc_commit(bar(Lay::B_SFULL + s));
-            if (!it.two || s == 1) tc_commit(bar(Lay::B_KVEMPTY + slot));
-            // the row tile of q is free after its last S
-            if (it.two ? j == nj - 1 : u == units - 1) tc_commit(bar(Lay::B_QEMPTY + qslot));
-          }
-          __syncwarp();
+        x = it.next;
+        if (it.j0 >= it.j1) continue;
+        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
+        int units = unit_count(it);
+        while (!unit_at(it, units - 1).live) --units;
+        auto left_of = [&](int j) { return it.len - (it.j0 + j) * kBN; };  // keys from the tile's first on
+        // whether the unit is the last of its tile
+        auto ends = [&](const Unit& un, int u) {
+          return (un.half == 1 || left_of(un.j) <= kHalf) && (!it.two || (u & 1));
         };
-        issue_s(0);
-        if (ok && units > 1) issue_s(1);
-        for (int u = 0; u < units && ok; ++u) {
-          const int j = it.two ? u >> 1 : u, s = u & 1;
-          const uint32_t n = n_ld + v_pos(j, nj, lead), slot = n % NS;
-          const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE;
-          const int left = it.len - (it.j0 + j) * kBN;  // keys of the tile inside the sequence, or more
-          const int steps = min(kBN / Lay::KSTEP, ceil_div(left, Lay::KSTEP));
-          if (!it.two || s == 0) {
-            ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
-            if (!ok) break;
-            tc_fence_after();
-            if (left < steps * Lay::KSTEP) {
-              // Rows behind the sequence's end that the last K step would multiply: whatever
-              // the page holds there must not meet the zero weights.
-              constexpr int U = Lay::ROWB / 16;
-              const int rows = steps * Lay::KSTEP - left;
-              for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
-                const int c = i / (rows * U), w = i - c * rows * U;
-                *reinterpret_cast<uint4*>(smem + Lay::KV_OFF + slot * Lay::TILE + c * Lay::CHUNK + left * Lay::ROWB + w * 16) =
-                    make_uint4(0, 0, 0, 0);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
+        if (warp == 9) {
+          constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, kHalf, 0, 0) : idesc_bf16_f32(kBM, kHalf, 0, 0);
+          auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
+          for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k)
+            ok = wait(Lay::B_QFULL + ((nq + k) & 1), ((nq + k) >> 1) & 1, kSiteTQFull);
+          if (!ok) break;
+          for (int u = 0; u < units; ++u) {
+            const Unit un = unit_at(it, u);
+            if (!un.live) continue;
+            const int s = u & 1, buf = u & 3;
+            const uint32_t n = n_ld + k_pos(un.j, lead), slot = n % NS;
+            if (un.half == 0 && (!it.two || s == 0)) ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+            // the buffer's last P~ has been multiplied
+            if (ok && ((used >> buf) & 1u)) {
+              ok = wait(Lay::B_PVDONE + buf, (phases >> buf) & 1u, kSiteTPvDone);
+              phases ^= 1u << buf;
             }
-          }
-          const uint32_t tS = tmem + (s ? Lay::TM_S1 : Lay::TM_S0), tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
-          uint32_t& ph = s ? p_phase1 : p_phase0;
-          const bool start = u < 2;  // the stream's first product
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = wait(Lay::B_PFULL + 2 * s + half, ph, kSiteTPFull);
             if (!ok) break;
+            used |= 1u << buf;
             tc_fence_after();
+            const int qslot = (nq + (it.two ? s : 0)) & 1;
+            const uint32_t tS = tmem + Lay::TM_S + 64 * buf;
+            const bool done = ends(un, u);
             if (elect_one()) {
-              constexpr int NK = kBN / Lay::KSTEP;
-              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
+              const uint64_t db0 = desc(sb + Lay::KV_OFF + slot * Lay::TILE + un.half * kHalf * Lay::ROWB);
+              const uint64_t dq0 = desc(sb + Lay::Q_OFF + qslot * Lay::QTILE);
 #pragma unroll
-              for (int kk = half * NK / 2; kk < (half + 1) * NK / 2; ++kk) {
-                if (kk >= steps) continue;
-                const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
-                const uint32_t acc = (!start || kk > 0) ? 1u : 0u;
-                if constexpr (F8) {
-                  mma_ts_f8(tO, tS + kk * 8, dv, idesc_o, acc);
-                  mma_ts_f8(tO, tS + 32 + kk * 8, dv, idesc_o, 1u);
-                } else {
-                  mma_ts(tO, tS + kk * 8, dv, idesc_o, acc);
+              for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+                const uint64_t da0 = desc_add(dq0, term * Lay::TILE);
+                constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
+#pragma unroll
+                for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
+                  const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
+                  const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
+                  if constexpr (F8) mma_ss_f8(tS, desc_add(da0, off), desc_add(db0, off), idesc, acc);
+                  else mma_ss(tS, desc_add(da0, off), desc_add(db0, off), idesc, acc);
                 }
+              }
+              tc_commit(bar(Lay::B_SFULL + buf));
+              if (done) tc_commit(bar(Lay::B_KVEMPTY + slot));
+              if (u == units - 1) {  // q is free after the item's last S
+                tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
+                if (it.two) tc_commit(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
               }
             }
             __syncwarp();
           }
-          if (!ok) break;
-          ph ^= 1u;
-          if (elect_one()) {
-            if (!it.two || s == 1) tc_commit(bar(Lay::B_KVEMPTY + slot));
-            if (u == units - 1) tc_commit(bar(Lay::B_OFULL));
+        } else {
+          constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
+          for (int u = 0; u < units; ++u) {
+            const Unit un = unit_at(it, u);
+            if (!un.live) continue;
+            const int s = u & 1, buf = u & 3;
+            const uint32_t n = n_ld + v_pos(un.j, nj, lead), slot = n % NS;
+            const int left = left_of(un.j) - un.half * kHalf;  // keys of the half inside the sequence, or more
+            constexpr int NK = kHalf / Lay::KSTEP;
+            const int steps = min(NK, ceil_div(left, Lay::KSTEP));
+            if (!it.two || s == 0) {
+              if (un.half == 0) {
+                ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+                if (!ok) break;
+              }
+              if (left < steps * Lay::KSTEP) {
+                // Rows behind the sequence's end that the last K step would multiply: whatever
+                // the page holds there must not meet the zero weights.
+                constexpr int U = Lay::ROWB / 16;
+                const int rows = steps * Lay::KSTEP - left;
+                uint8_t* at = smem + Lay::KV_OFF + slot * Lay::TILE + (un.half * kHalf + left) * Lay::ROWB;
+                for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
+                  const int c = i / (rows * U), w = i - c * rows * U;
+                  *reinterpret_cast<uint4*>(at + c * Lay::CHUNK + w * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+            ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
+            if (!ok) break;
+            phases ^= 1u << buf;
+            tc_fence_after();
+            const uint32_t tP = tmem + Lay::TM_S + 64 * buf, tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
+            const uint32_t more = u >= 2 ? 1u : 0u;  // not the stream's first product
+            const bool done = ends(un, u);
+            if (elect_one()) {
+              const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE + un.half * kHalf * Lay::ROWB;
+              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
+#pragma unroll
+              for (int kk = 0; kk < NK; ++kk) {
+                if (kk >= steps) continue;
+                const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
+                const uint32_t acc = kk > 0 ? 1u : more;
+                if constexpr (F8) {
+                  mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
+                  mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
+                } else {
+                  mma_ts(tO, tP + kk * 8, dv, idesc, acc);
+                }
+              }
+              tc_commit(bar(Lay::B_PVDONE + buf));
+              if (done) tc_commit(bar(Lay::B_KVEMPTY + slot));
+              if (u == units - 1) tc_commit(bar(Lay::B_OFULL));
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          if (u + 2 < units) issue_s(u + 2);
         }
         n_ld += 2u * nj;
         nq += it.two ? 2 : 1;
       }
       // Every product issued by this warp completes before TMEM is freed.
-      if (elect_one()) tc_commit(bar(Lay::B_DRAIN));
+      const int db = Lay::B_DRAIN + (warp == 9 ? 0 : 1);
+      if (elect_one()) tc_commit(bar(db));
       __syncwarp();
-      if (!__all_sync(0xffffffffu, drain_wait(bar(Lay::B_DRAIN), 0u, kDrainLimitNs)) && lane == 0 && p.err)
+      if (!__all_sync(0xffffffffu, drain_wait(bar(db), 0u, kDrainLimitNs)) && lane == 0 && p.err)
         atomicCAS(p.err, 0, timeout_code(kSiteTDrain));
-    } else if (F8) {
-      // ------------------------------------------------- split queries (E4M3)
-      // Warps 10 and 11 take every other row: scale by a power of two that brings the row's
-      // largest value into [128, 256), hi = E4M3(x), lo = E4M3(x - hi).
-      int nq = 0;
-      bool ok = true;
-      float* qs = reinterpret_cast<float*>(smem + Lay::QS_OFF);
-      for (int x = x0; x < x1 && ok;) {
-        const Seg it = list.at(x, x1);
-        x += it.j1 - it.j0;
-        for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
-          const int slot = nq & 1;
-          if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
-          if (!ok) break;
-          const int rows = (it.two ? (k ? it.nt - p.tpt : p.tpt) : it.nt) * p.G;
-          const int64_t tok = it.q0 + it.tok0 + k * p.tpt;
-          uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
-          // A row is held by D / 8 lanes, 8 values each.
-          constexpr int L = D / 8, R = 32 / L;
-          for (int r0 = (warp - 10) * R; r0 < rows; r0 += 2 * R) {
-            const int r = r0 + lane / L, c = lane % L;
-            const bool live = r < rows;
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (live) {
-              const int t = r / p.G, gg = r - t * p.G;
-              w = __ldg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
-            }
-            float v[8];
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] = __uint_as_float(u[i] << 16);
-              v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-              top = fmaxf(top, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
-            }
-#pragma unroll
-            for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
-            int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-            e = max(-100, min(e, 120));
-            const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-            if (live && c == 0) qs[slot * kBM + r] = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              hi[i] = lo[i] = 0;
-#pragma unroll
-              for (int k2 = 0; k2 < 2; ++k2) {
-                const float a = v[4 * i + 2 * k2] * up, b = v[4 * i + 2 * k2 + 1] * up;
-                const float ha = upper4(a), hb = upper4(b);
-                hi[i] |= pack_e4m3x2(ha, hb) << (16 * k2);
-                lo[i] |= pack_e4m3x2(a - ha, b - hb) << (16 * k2);
-              }
-            }
-            if (live) {
-              // 16-byte units of a row are permuted as the copies' swizzle does.
-              const int unit = c >> 1;
-              const int at = Lay::ROWB == 128 ? r * 128 + ((unit ^ (r & 7)) << 4) : r * 64 + ((unit ^ ((r >> 1) & 3)) << 4);
-              *reinterpret_cast<uint2*>(base + at + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(base + Lay::TILE + at + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Lay::B_QFULL + slot));
-        }
-      }
     }
   }
 
-  // The item whose first tiles this CTA holds without its last ones.
-  if (threadIdx.x == 0) {
-    int4 hd = make_int4(-1, 0, 0, 0);
-    if (x1 > x0) {
-      const Seg it = list.at(x1 - 1, x1);
-      const int begin = x1 - 1 - it.j0;  // position of the item's first tile
-      if (begin >= x0 && begin + it.kvt > x1) {
-        int last = static_cast<int>((static_cast<int64_t>(begin + it.kvt - 1) * ctas) / total);
-        while (static_cast<int64_t>(last + 1) * total / ctas <= begin + it.kvt - 1) ++last;
-        while (static_cast<int64_t>(last) * total / ctas > begin + it.kvt - 1) --last;
-        hd = make_int4(it.q0 + it.tok0, it.h, it.nt, last);
-      }
-    }
-    p.head[cta] = hd;
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -869,67 +922,66 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of the items that were split: CTA c's second slot holds the first part, the
-// first slots of CTAs c + 1 .. last the others, in the order of the keys.  A warp per row.
+// first slots of CTAs c + 1 .. last the others, in the order of the keys.  A thread joins four
+// columns of a row, eight parts at a time.
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int c = blockIdx.x;
   const int4 hd = p.head[c];
   if (hd.x < 0) return;
-  const int i = blockIdx.y * 4 + (threadIdx.x >> 5);  // token i / G, head i % G
-  if (i >= hd.z * p.G) return;
-  const int t = i / p.G, g = i - t * p.G;
+  const int rows = hd.z * p.G;
+  const int i = blockIdx.y * 128 + threadIdx.x;
+  const int col = i / rows, j = i - col * rows;  // columns 4 col.., row j: token j / G, head j % G
+  if (col >= D / 4) return;
+  const int t = j / p.G, g = j - t * p.G;
   const int tile = t / p.tpt;
   const int r = tile * kBM + (t - tile * p.tpt) * p.G + g;
   const int parts = hd.w - c + 1;
-  auto at = [&](int k) -> int64_t { return (static_cast<int64_t>(c + k) * 2 + (k == 0 ? 1 : 0)) * (2 * kBM) + r; };
-  float m = -INFINITY;
-  for (int k = lane; k < parts; k += 32) m = fmaxf(m, p.stat[at(k)].x);
+  constexpr int N = 8;
+  float m = -INFINITY, l = 0.f, acc[4] = {};
+  for (int k0 = 0; k0 < parts; k0 += N) {
+    float2 st[N];
+    float4 v[N];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  constexpr int E = D / 32;
-  float acc[E] = {}, l = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    float w = 0.f, lk = 0.f;
-    if (k0 + lane < parts) {
-      const float2 st = p.stat[at(k0 + lane)];
-      w = st.x == -INFINITY ? 0.f : fast_exp2(st.x - m);
-      lk = st.y;
+    for (int k = 0; k < N; ++k) {
+      st[k] = make_float2(-INFINITY, 0.f);
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < parts) {
+        const int64_t slot = static_cast<int64_t>(c + k0 + k) * 2 + (k0 + k == 0 ? 1 : 0);
+        st[k] = p.stat[slot * (2 * kBM) + r];
+        v[k] = reinterpret_cast<const float4*>(p.part)[(slot * (D / 4) + col) * (2 * kBM) + r];
+      }
     }
-    const int n = min(32, parts - k0);
-    for (int k = 0; k < n; k += 4) {
-      float v[4][E];
+    float top = m;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float* src = p.part + at(k0 + min(k + q, n - 1)) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(src);
-          v[q][0] = f.x; v[q][1] = f.y; v[q][2] = f.z; v[q][3] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(src);
-          v[q][0] = f.x; v[q][1] = f.y;
-        }
-      }
+    for (int k = 0; k < N; ++k) top = fmaxf(top, st[k].x);
+    if (top == -INFINITY) continue;  // no key of these parts is seen
+    const float old = fast_exp2(m - top);
+    m = top;
+    l *= old;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float wk = __shfl_sync(0xffffffffu, w, (k + q) & 31), lq = __shfl_sync(0xffffffffu, lk, (k + q) & 31);
-        if (k + q < n && wk != 0.f) {
-          l = fmaf(wk, lq, l);
+    for (int e = 0; e < 4; ++e) acc[e] *= old;
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(wk, v[q][e], acc[e]);
-        }
-      }
+    for (int k = 0; k < N; ++k) {
+      const float w = st[k].x == -INFINITY ? 0.f : fast_exp2(st[k].x - m);
+      if (w == 0.f) continue;
+      l = fmaf(w, st[k].y, l);
+      acc[0] = fmaf(w, v[k].x, acc[0]);
+      acc[1] = fmaf(w, v[k].y, acc[1]);
+      acc[2] = fmaf(w, v[k].z, acc[2]);
+      acc[3] = fmaf(w, v[k].w, acc[3]);
     }
   }
   const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
   const int64_t row = static_cast<int64_t>(hd.x + t) * p.Hq + hd.y * p.G + g;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.o + row * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) dst[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-  if (lane == 0)
+  *reinterpret_cast<uint2*>(p.o + row * D + 4 * col) =
+      make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  if (col == 0)
     p.lse[static_cast<int64_t>(hd.y * p.G + g) * p.T + hd.x + t] = l > 0.f ? (m + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
 }
 
+constexpr int kMaxSmem = 232448;
 constexpr int kMaxGrid = 160;  // CTAs the workspace has room for (148 SMs)
 
 template <int D, bool F8>
@@ -938,13 +990,22 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
   using Lay = Layout<D, F8>;
   auto kern = tree_kernel<D, F8>;
   const int smem = 1024 + Lay::TABLE_OFF + (4 * p.B + 2) * 4;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static_assert(1024 + Lay::TABLE_OFF + (4 * 1024 + 2) * 4 <= kMaxSmem, "tables of 1024 sequences fit");
+  // Once per device: the call costs the host more than a tensor map does.
+  static std::atomic<uint64_t> ready{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (!((ready.load(std::memory_order_acquire) >> dev) & 1)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
   kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (rows + 3) / 4, 1);
+  cfg.gridDim = dim3(grid, (rows * (D / 4) + 127) / 128, 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1007,7 +1068,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   // describe.
   const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
   const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
-  if (items > INT32_MAX / tiles) return ATTN_ERR_UNSUPPORTED;
+  if (items > INT32_MAX / (4 * tiles)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
   int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
   if (grid > kMaxGrid) grid = kMaxGrid;
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
