@@ -791,117 +791,136 @@ __global__ void __launch_bounds__(kThreads, 1)
         x = it.next;
         if (it.j0 >= it.j1) continue;
         const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
-        int units = unit_count(it);
-        while (!unit_at(it, units - 1).live) --units;
-        auto left_of = [&](int j) { return it.len - (it.j0 + j) * kBN; };  // keys from the tile's first on
-        // whether the unit is the last of its tile
-        auto ends = [&](const Unit& un, int u) {
-          return (un.half == 1 || left_of(un.j) <= kHalf) && (!it.two || (u & 1));
-        };
+        const int steps2 = unit_count(it) >> 2;  // pairs of tiles (one row tile) or tiles (two)
+        auto halves = [&](int j) { return it.len - (it.j0 + j) * kBN > kHalf ? 2 : 1; };
         if (warp == 9) {
           constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, kHalf, 0, 0) : idesc_bf16_f32(kBM, kHalf, 0, 0);
           auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
           for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k)
             ok = wait(Lay::B_QFULL + ((nq + k) & 1), ((nq + k) >> 1) & 1, kSiteTQFull);
-          if (!ok) break;
-          for (int u = 0; u < units; ++u) {
-            const Unit un = unit_at(it, u);
-            if (!un.live) continue;
-            const int s = u & 1, buf = u & 3;
-            const uint32_t n = n_ld + k_pos(un.j, lead), slot = n % NS;
-            if (un.half == 0 && (!it.two || s == 0)) ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
-            // the buffer's last P~ has been multiplied
-            if (ok && ((used >> buf) & 1u)) {
-              ok = wait(Lay::B_PVDONE + buf, (phases >> buf) & 1u, kSiteTPvDone);
-              phases ^= 1u << buf;
-            }
-            if (!ok) break;
-            used |= 1u << buf;
-            tc_fence_after();
-            const int qslot = (nq + (it.two ? s : 0)) & 1;
-            const uint32_t tS = tmem + Lay::TM_S + 64 * buf;
-            const bool done = ends(un, u);
-            if (elect_one()) {
-              const uint64_t db0 = desc(sb + Lay::KV_OFF + slot * Lay::TILE + un.half * kHalf * Lay::ROWB);
-              const uint64_t dq0 = desc(sb + Lay::Q_OFF + qslot * Lay::QTILE);
+          const uint64_t dq0 = desc(sb + Lay::Q_OFF + (nq & 1) * Lay::QTILE);
+          const uint64_t dq1 = it.two ? desc(sb + Lay::Q_OFF + ((nq + 1) & 1) * Lay::QTILE) : dq0;
+          // The units of both streams for one half: one round of waits, then all their products.
+          for (int v = 0; v < steps2 && ok; ++v) {
+            const int ja = it.two ? v : 2 * v, jb = it.two ? v : 2 * v + 1;
+            const uint32_t na = n_ld + k_pos(ja, lead), nb = n_ld + k_pos(jb, lead);
+            const uint32_t sa = na % NS, sbl = nb % NS;
+            const int ha = halves(ja), hb = jb < nj ? halves(jb) : 0;
+            ok = wait(Lay::B_KVFULL + sa, (na / NS) & 1u, kSiteTKvFull);
+            if (ok && !it.two && hb) ok = wait(Lay::B_KVFULL + sbl, (nb / NS) & 1u, kSiteTKvFull);
+            for (int half = 0; half < ha && ok; ++half) {  // the second tile is no fuller than the first
+              const bool b_too = half < hb;
+              const int b0 = 2 * half, b1 = b0 + 1;
+              // the buffers' last P~ have been multiplied
+              if ((used >> b0) & 1u) {
+                ok = wait(Lay::B_PVDONE + b0, (phases >> b0) & 1u, kSiteTPvDone);
+                phases ^= 1u << b0;
+              }
+              if (ok && b_too && ((used >> b1) & 1u)) {
+                ok = wait(Lay::B_PVDONE + b1, (phases >> b1) & 1u, kSiteTPvDone);
+                phases ^= 1u << b1;
+              }
+              if (!ok) break;
+              used |= (b_too ? 3u : 1u) << b0;
+              tc_fence_after();
+              const uint64_t dka = desc(sb + Lay::KV_OFF + sa * Lay::TILE + half * kHalf * Lay::ROWB);
+              const uint64_t dkb = desc(sb + Lay::KV_OFF + sbl * Lay::TILE + half * kHalf * Lay::ROWB);
+              const uint32_t tS = tmem + Lay::TM_S + 64 * b0;
+              const bool last = v == steps2 - 1 && half == ha - 1;
+              if (elect_one()) {
+                auto products = [&](uint32_t d, uint64_t dq, uint64_t dk) {
+                  constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
 #pragma unroll
-              for (int term = 0; term < (F8 ? 2 : 1); ++term) {
-                const uint64_t da0 = desc_add(dq0, term * Lay::TILE);
-                constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
+                  for (int term = 0; term < (F8 ? 2 : 1); ++term)
 #pragma unroll
-                for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
-                  const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
-                  const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
-                  if constexpr (F8) mma_ss_f8(tS, desc_add(da0, off), desc_add(db0, off), idesc, acc);
-                  else mma_ss(tS, desc_add(da0, off), desc_add(db0, off), idesc, acc);
+                    for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
+                      const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
+                      const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
+                      if constexpr (F8) mma_ss_f8(d, desc_add(dq, off + term * Lay::TILE), desc_add(dk, off), idesc, acc);
+                      else mma_ss(d, desc_add(dq, off), desc_add(dk, off), idesc, acc);
+                    }
+                };
+                products(tS, dq0, dka);
+                tc_commit(bar(Lay::B_SFULL + b0));
+                if (!it.two && half == ha - 1) tc_commit(bar(Lay::B_KVEMPTY + sa));
+                if (b_too) {
+                  products(tS + 64, dq1, dkb);
+                  tc_commit(bar(Lay::B_SFULL + b1));
+                  if (half == hb - 1) tc_commit(bar(Lay::B_KVEMPTY + sbl));
+                }
+                if (last) {  // q is free after the item's last S
+                  tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
+                  if (it.two) tc_commit(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
                 }
               }
-              tc_commit(bar(Lay::B_SFULL + buf));
-              if (done) tc_commit(bar(Lay::B_KVEMPTY + slot));
-              if (u == units - 1) {  // q is free after the item's last S
-                tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
-                if (it.two) tc_commit(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
-              }
+              __syncwarp();
             }
-            __syncwarp();
           }
+          if (!ok) break;
         } else {
           constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
-          for (int u = 0; u < units; ++u) {
-            const Unit un = unit_at(it, u);
-            if (!un.live) continue;
-            const int s = u & 1, buf = u & 3;
-            const uint32_t n = n_ld + v_pos(un.j, nj, lead), slot = n % NS;
-            const int left = left_of(un.j) - un.half * kHalf;  // keys of the half inside the sequence, or more
-            constexpr int NK = kHalf / Lay::KSTEP;
-            const int steps = min(NK, ceil_div(left, Lay::KSTEP));
-            if (!it.two || s == 0) {
-              if (un.half == 0) {
-                ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
-                if (!ok) break;
-              }
-              if (left < steps * Lay::KSTEP) {
-                // Rows behind the sequence's end that the last K step would multiply: whatever
-                // the page holds there must not meet the zero weights.
-                constexpr int U = Lay::ROWB / 16;
-                const int rows = steps * Lay::KSTEP - left;
-                uint8_t* at = smem + Lay::KV_OFF + slot * Lay::TILE + (un.half * kHalf + left) * Lay::ROWB;
-                for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
-                  const int c = i / (rows * U), w = i - c * rows * U;
-                  *reinterpret_cast<uint4*>(at + c * Lay::CHUNK + w * 16) = make_uint4(0, 0, 0, 0);
+          constexpr int NK = kHalf / Lay::KSTEP;
+          for (int v = 0; v < steps2 && ok; ++v) {
+            const int ja = it.two ? v : 2 * v, jb = it.two ? v : 2 * v + 1;
+            const int ha = halves(ja), hb = jb < nj ? halves(jb) : 0;
+            for (int half = 0; half < ha && ok; ++half) {
+              for (int s = 0; s < 2; ++s) {
+                if (s == 1 && half >= hb) continue;
+                const int j = s ? jb : ja, buf = 2 * half + s;
+                const uint32_t n = n_ld + v_pos(j, nj, lead), slot = n % NS;
+                const int left = it.len - (it.j0 + j) * kBN - half * kHalf;  // keys of the half inside the sequence, or more
+                const int steps = min(NK, ceil_div(left, Lay::KSTEP));
+                if (!it.two || s == 0) {
+                  if (half == 0) {
+                    ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+                    if (!ok) break;
+                  }
+                  if (left < steps * Lay::KSTEP) {
+                    // Rows behind the sequence's end that the last K step would multiply:
+                    // whatever the page holds there must not meet the zero weights.
+                    constexpr int U = Lay::ROWB / 16;
+                    const int rows = steps * Lay::KSTEP - left;
+                    uint8_t* at = smem + Lay::KV_OFF + slot * Lay::TILE + (half * kHalf + left) * Lay::ROWB;
+                    for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
+                      const int c = i / (rows * U), w = i - c * rows * U;
+                      *reinterpret_cast<uint4*>(at + c * Lay::CHUNK + w * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                  }
                 }
-                fence_proxy_async_smem();
+                ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
+                if (!ok) break;
+                phases ^= 1u << buf;
+                tc_fence_after();
+                const uint32_t tP = tmem + Lay::TM_S + 64 * buf, tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
+                const uint32_t more = (v > 0 || half > 0) ? 1u : 0u;  // not the stream's first product
+                const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE + half * kHalf * Lay::ROWB;
+                const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
+                const bool tile_ends = half == (s ? hb : ha) - 1 && (!it.two || s == 1);
+                const bool last = v == steps2 - 1 && half == ha - 1 && (s == 1 || half >= hb);
+                if (elect_one()) {
+#pragma unroll
+                  for (int kk = 0; kk < NK; ++kk) {
+                    if (kk >= steps) continue;
+                    const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
+                    const uint32_t acc = kk > 0 ? 1u : more;
+                    if constexpr (F8) {
+                      mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
+                      mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
+                    } else {
+                      mma_ts(tO, tP + kk * 8, dv, idesc, acc);
+                    }
+                  }
+                  tc_commit(bar(Lay::B_PVDONE + buf));
+                  if (tile_ends) tc_commit(bar(Lay::B_KVEMPTY + slot));
+                  if (last) tc_commit(bar(Lay::B_OFULL));
+                }
                 __syncwarp();
               }
             }
-            ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
-            if (!ok) break;
-            phases ^= 1u << buf;
-            tc_fence_after();
-            const uint32_t tP = tmem + Lay::TM_S + 64 * buf, tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
-            const uint32_t more = u >= 2 ? 1u : 0u;  // not the stream's first product
-            const bool done = ends(un, u);
-            if (elect_one()) {
-              const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE + un.half * kHalf * Lay::ROWB;
-              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
-#pragma unroll
-              for (int kk = 0; kk < NK; ++kk) {
-                if (kk >= steps) continue;
-                const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
-                const uint32_t acc = kk > 0 ? 1u : more;
-                if constexpr (F8) {
-                  mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
-                  mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
-                } else {
-                  mma_ts(tO, tP + kk * 8, dv, idesc, acc);
-                }
-              }
-              tc_commit(bar(Lay::B_PVDONE + buf));
-              if (done) tc_commit(bar(Lay::B_KVEMPTY + slot));
-              if (u == units - 1) tc_commit(bar(Lay::B_OFULL));
-            }
-            __syncwarp();
           }
+          if (!ok) break;
         }
         n_ld += 2u * nj;
         nq += it.two ? 2 : 1;
