@@ -52,7 +52,8 @@ constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 enum TreeSite : int {  // wait sites of the device error word (16..30)
   kSiteTQFull = 16, kSiteTQEmpty, kSiteTKvFull, kSiteTKvEmpty, kSiteTSFull, kSiteTPFull, kSiteTOFull, kSiteTMerge,
-  kSiteTDrain, kSiteTPvDone
+  kSiteTDrain, kSiteTPvDone, kSiteTSFree,
+  kSiteTItems
 };
 __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
 
@@ -69,6 +70,7 @@ struct TreeParams {
   int rows;        // rows of the tensor maps: a copy from there on gives zeros
   int box_rows;    // rows of one K/V copy: min(page size, 128)
   int tpt;         // tokens of a 128-row tile: 128 / G
+  int tpt64;       // tokens of 64 rows: 64 / G
   float scale_log2, o_scale, tau, p_shift;
   float* part;     // [grid][2][D / 4][256][4] unnormalised O: four columns of neighbouring rows
                    // lie together, as the lanes that write and join them are neighbouring rows
@@ -88,22 +90,40 @@ struct Layout {
   static constexpr int TILE = NCHUNK * CHUNK;
   static constexpr int CELEMS = ROWB / ESZ;  // values of a row in a chunk
   static constexpr int KSTEP = 32 / ESZ;     // values of a K step of the products
-  static constexpr int NSTAGE = TILE >= 32768 ? 4 : 8;
+  // Two rings, K's slots first: each has one producer and one consumer that take its slots in
+  // order, so that no role is ever a whole round ahead of a barrier's parity.
+  static constexpr int NRING = TILE >= 32768 ? 2 : 4;
+  static constexpr int NSTAGE = 2 * NRING;
   static constexpr int QTILE = F8 ? 2 * TILE : TILE;  // E4M3: hi, then lo
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = 2 * QTILE;
-  static constexpr int ML_OFF = KV_OFF + NSTAGE * TILE;      // float2 [2][128]: (m, l) of the two streams
-  static constexpr int QS_OFF = ML_OFF + 2 * kBM * 8;        // float [2][128]: 1 / scale of the split queries
-  static constexpr int BAR_OFF = QS_OFF + 2 * kBM * 4;
+  // P~ of swapped items, [128 keys][128 bytes] per stream.  With d = 128 it lies where a tile of q
+  // keeps rows that swapped items do not have: see p_row.
+  static constexpr int P_OFF = KV_OFF + NSTAGE * TILE;
+  static constexpr int ML_OFF = P_OFF + (D == 64 ? 2 * 16384 : 0);  // float2 [2][128]: (m, l) of the two streams
+  static constexpr int QS_OFF = ML_OFF + 2 * kBM * 8;  // float [2][128]: factors of the scores (split queries)
+  // swapped items, per stream: -m_ref + p_shift, rescale factors, m_ref, (row sums by warp, then the
+  // weights of the streams): float [64] each, the last [4][64]; then four vote flags
+  static constexpr int SW_OFF = QS_OFF + 2 * kBM * 4;
+  static constexpr int SW_STREAM = 7 * 64 + 4;
+  static constexpr int BAR_OFF = SW_OFF + 2 * SW_STREAM * 4;
   // SFULL, PFULL, PVDONE: one per S buffer; DRAIN: one per issuing warp
+  // The W forms are those of swapped items, one per stream; WG: the four warps of a stream.
   static constexpr int B_QFULL = 0, B_QEMPTY = 2, B_SFULL = 4, B_PFULL = 8, B_PVDONE = 12, B_OFULL = 16, B_ML = 17,
-                       B_EPI = 18, B_DRAIN = 19, B_KVFULL = 21, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
+                       B_EPI = 18, B_DRAIN = 19, B_WSFULL = 21, B_WSFREE = 23, B_WPFULL = 25, B_WPVDONE = 27, B_WG = 29,
+                       B_KVFULL = 31, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int TABLE_OFF = MISC_OFF + 128;
   // Cost of a key tile with one and with two row tiles: the copies bound the first, the softmax
   // of 256 rows the second.
   static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 1, COST_PAIR = ESZ * D == 256 ? 4 : 2;
-  static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 256 + D;  // S: four buffers of 64 columns
+  static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
+  // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
+  __host__ __device__ static constexpr int p_row(int s, int key) {
+    return D == 64 ? P_OFF + s * 16384 + key * 128
+           : F8    ? Q_OFF + s * QTILE + TILE + key * 128
+                   : Q_OFF + s * QTILE + (key >> 6) * CHUNK + 64 * 128 + (key & 63) * 128;
+  }
 };
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
@@ -116,6 +136,7 @@ struct Seg {
   int j0, j1, kvt;
   int begin, next;        // where the item begins in the list, and the next stretch
   bool two;               // more than one row tile
+  bool swapped;           // at most 64 rows
 };
 
 // The list of work, decoded alike by every role: items (sequence, cache head, row pair) one
@@ -125,7 +146,7 @@ struct Seg {
 // sequence: cum (cost before it), first row of q, slot, tokens in the cache.
 struct List {
   const int *cum, *cu, *slot, *len;
-  int B, heads, tpt, one, pair;
+  int B, heads, G, tpt, one, pair;
   bool masked;
 
   // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
@@ -161,6 +182,7 @@ struct List {
     s.tok0 = rt * 2 * tpt;
     s.nt = min(2 * tpt, s.n - s.tok0);
     s.two = s.nt > tpt;
+    s.swapped = s.nt * G <= 64;
     s.kvt = kv;
     s.begin = x - r;
     s.next = min(end, s.begin + kv * w);
@@ -192,11 +214,6 @@ __device__ __forceinline__ int unit_count(const Seg& it) {
   return 4 * (it.two ? nj : (nj + 1) / 2);
 }
 
-// The order of K and V tiles in the ring: K runs `lead` tiles ahead of V (two row tiles: 1,
-// one: 2, a tile of each stream).
-__device__ __forceinline__ int k_pos(int j, int lead) { return j + max(0, j - lead + 1); }
-__device__ __forceinline__ int v_pos(int j, int n, int lead) { return j + min(n, j + lead); }
-
 __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(bar, parity)) {
@@ -220,17 +237,18 @@ __device__ __forceinline__ uint32_t below(int k, int g) {
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ TreeParams p) {
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q64,
+                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                const __grid_constant__ TreeParams p) {
   using Lay = Layout<D, F8>;
-  constexpr int NS = Lay::NSTAGE;
+  constexpr int NS = Lay::NSTAGE, NR = Lay::NRING;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sb + Lay::BAR_OFF + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::MISC_OFF);
-  // misc[0] TMEM base, misc[1] abort flag, misc[4..16) sums of the warps
+  // misc[0] TMEM base, misc[1] abort flag, misc[2] items finished, misc[4..16) sums of the warps
   int* tab = reinterpret_cast<int*>(smem + Lay::TABLE_OFF);
   int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -241,6 +259,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Lay::B_QFULL + s), F8 ? 8 : 1);  // E4M3: written by the softmax warps
       mbar_init(bar(Lay::B_QEMPTY + s), 1);
       mbar_init(bar(Lay::B_DRAIN + s), 1);
+      mbar_init(bar(Lay::B_WSFULL + s), 1);
+      mbar_init(bar(Lay::B_WSFREE + s), 4);
+      mbar_init(bar(Lay::B_WPFULL + s), 4);
+      mbar_init(bar(Lay::B_WPVDONE + s), 1);
+      mbar_init(bar(Lay::B_WG + s), 4);
+      int* votes = reinterpret_cast<int*>(smem + Lay::SW_OFF) + s * Lay::SW_STREAM + 7 * 64;
+      for (int i = 0; i < 4; ++i) votes[i] = 0;
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(Lay::B_SFULL + i), 1);
@@ -254,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Lay::B_KVFULL + i), 1);
       mbar_init(bar(Lay::B_KVEMPTY + i), 1);
     }
-    misc[1] = 0u;
+    misc[1] = misc[2] = 0u;
     fence_barrier_init();
   }
   if (warp == 9) {
@@ -268,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   list.len = t_len;
   list.B = p.B;
   list.heads = p.heads;
+  list.G = p.G;
   list.tpt = p.tpt;
   list.one = Lay::COST_ONE;
   list.pair = Lay::COST_PAIR;
@@ -345,6 +371,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, wc, timeout_code(site)));
   };
 
+  // Until this CTA has finished its first k items.  A count, not a barrier's phase: the waiting
+  // role may be several items ahead.
+  auto wait_items = [&](int k) -> bool {
+    const uint32_t at = sb + Lay::MISC_OFF + 8;
+    const uint64_t t0 = global_timer_ns();
+    bool good = true;
+    while (true) {
+      uint32_t done;
+      asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(done) : "r"(at) : "memory");
+      if (static_cast<int>(done) >= k) break;
+      if (*wc.abort) good = false;
+      if (good && global_timer_ns() - t0 > wc.limit_ns) {
+        *wc.abort = 1u;
+        if (wc.err) atomicCAS(wc.err, 0, timeout_code(kSiteTItems));
+        good = false;
+      }
+      if (!good) break;
+    }
+    return __all_sync(0xffffffffu, good);
+  };
   // E4M3: softmax warp w writes its eighth of an item's queries, from q slot nq on: each row is
   // scaled by the power of two that brings its largest value into [128, 256), hi = E4M3(x), lo =
   // E4M3(x - hi).
@@ -399,12 +445,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (r < rows) {
-            if (c == 0) qs[slot * kBM + r] = __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-            // 16-byte units of a row are permuted as the copies' swizzle does.
-            const int unit = c >> 1;
-            const int at = Lay::ROWB == 128 ? r * 128 + ((unit ^ (r & 7)) << 4) : r * 64 + ((unit ^ ((r >> 1) & 3)) << 4);
-            *reinterpret_cast<uint2*>(base + at + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(base + Lay::TILE + at + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+            if (c == 0)
+              qs[slot * kBM + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+            // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
+            // lo rows follow its hi rows: both are columns of one product.
+            auto at = [&](int row) {
+              return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
+                                      : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
+            };
+            uint8_t* lo_at = it.swapped ? base + at(r + (rows + 15) / 16 * 16) : base + Lay::TILE + at(r);
+            *reinterpret_cast<uint2*>(base + at(r)) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
           }
         }
       }
@@ -429,6 +480,296 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phases = 0;  // bit u & 3: phase of that buffer's next use
     uint32_t o_phase = 0, m_phase = 0, e_phase = 0;
     int nq = 0;  // row tiles of q taken so far
+    int items = 0;
+    auto finished = [&]() {
+      ++items;
+      if (threadIdx.x == 0)
+        asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sb + Lay::MISC_OFF + 8), "r"(items) : "memory");
+    };
+    uint32_t w_s_phase = 0, w_pv = 0, w_wg = 0, votes = 0;  // swapped items; w_pv: P~ handed over
+    // An item of at most 64 rows, scores transposed: a thread holds one key of the tile and all
+    // rows, so all four warps of the stream share the exponentials, however few rows there are.
+    // P~ (rows side by side) goes to shared memory as the second operand of O^T += V^T P~^T.  The
+    // maximum of a row is over lanes and warps: it is taken for the stream's first tile, and again
+    // only when some score exceeds its row's reference by more than tau (a vote of the four warps).
+    auto swapped_item = [&](const Seg& it, int nq_item) -> bool {
+      const int nj = it.j1 - it.j0, rows = it.nt * p.G, nch = (rows + 15) >> 4;
+      const int key = r;
+      float* st = reinterpret_cast<float*>(smem + Lay::SW_OFF) + s * Lay::SW_STREAM;
+      float *nm = st, *al = st + 64, *mr = st + 128, *wm = st + 192;
+      volatile int* vote = reinterpret_cast<volatile int*>(st + 448);
+      const float* qs = reinterpret_cast<const float*>(smem + Lay::QS_OFF) + (nq_item & 1) * kBM;
+      const uint32_t t_s = tmem + lane_bits + Lay::TM_S + 128 * s;
+      auto meet = [&]() -> bool {  // the stream's four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::B_WG + s));
+        const bool good = wait(Lay::B_WG + s, w_wg & 1u, kSiteTMerge);
+        w_wg ^= 1u;
+        return good;
+      };
+      float l[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) l[i] = 0.f;
+      bool first = true;
+      for (int j = s; j < nj; j += 2) {
+        if (!wait(Lay::B_WSFULL + s, w_s_phase, kSiteTSFull)) return false;
+        w_s_phase ^= 1u;
+        tc_fence_after();
+        float x[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < nch) {
+            uint32_t w[16];
+            tmem_ld_x16(t_s + 16 * c, w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(w[i]);
+            if constexpr (F8) {
+              tmem_ld_x16(t_s + 16 * (nch + c), w);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[16 * c + i] += __uint_as_float(w[i]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::B_WSFREE + s));
+        // Rows that see this key.
+        const int pos = (it.j0 + j) * kBN + key, jl = pos - it.ctx;
+        uint32_t vis[2] = {below(rows, 0), below(rows, 1)};
+        const bool part = (it.j0 + j + 1) * kBN > it.ctx;
+        if (part && jl >= 0) {
+          uint32_t see[2] = {0u, 0u};
+          if (pos < it.len) {
+            if (p.mask == nullptr) {
+              const int from = max(0, jl - it.tok0) * p.G;  // tokens from jl on
+              see[0] = ~below(from, 0);
+              see[1] = ~below(from, 1);
+            } else {
+              const uint8_t* m = p.mask + static_cast<int64_t>(it.q0 + it.tok0) * p.mask_width + jl;
+#pragma unroll 4
+              for (int t2 = 0; t2 < it.nt; ++t2)
+                if (__ldg(m + static_cast<int64_t>(t2) * p.mask_width) != 0) {
+                  see[0] |= below((t2 + 1) * p.G, 0) & ~below(t2 * p.G, 0);
+                  see[1] |= below((t2 + 1) * p.G, 1) & ~below(t2 * p.G, 1);
+                }
+            }
+          }
+          vis[0] &= see[0];
+          vis[1] &= see[1];
+        }
+        if (part || (rows & 15)) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i < 16 * nch && !((vis[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
+        }
+        bool renew = first;
+        if (!first) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            if (c < 4 * nch) {
+              const float4 n4 = reinterpret_cast<const float4*>(nm)[c];
+              float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+              if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[c];
+              top = fmax3(top, fmaf(x[4 * c], s4.x, n4.x), fmaf(x[4 * c + 1], s4.y, n4.y));
+              top = fmax3(top, fmaf(x[4 * c + 2], s4.z, n4.z), fmaf(x[4 * c + 3], s4.w, n4.w));
+            }
+          }
+          const bool over = __any_sync(0xffffffffu, top > p.tau + p.p_shift);
+          if (over && lane == 0) vote[votes & 3] = 1;
+          if (!meet()) return false;
+          renew = vote[votes & 3] != 0;
+          if (wq == 0 && lane == 0) vote[(votes + 2) & 3] = 0;  // read by all before the last meeting
+          ++votes;
+        }
+        // P~ of the stream's last tile has been multiplied: O is whole, its place is free
+        if (w_pv > 0 && !wait(Lay::B_WPVDONE + s, (w_pv - 1) & 1u, kSiteTPvDone)) return false;
+        tc_fence_after();
+        if (renew) {
+          float keep[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            if (i < 16 * nch) {
+              float y = x[i] * (F8 ? qs[i] : p.scale_log2);
+#pragma unroll
+              for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
+              if (lane == (i & 31)) keep[i >> 5] = y;
+            }
+          }
+          wm[wq * 64 + lane] = keep[0];
+          wm[wq * 64 + 32 + lane] = keep[1];
+          if (!meet()) return false;
+          if (key < 64) {
+            const float m = fmaxf(fmaxf(wm[key], wm[64 + key]), fmaxf(wm[128 + key], wm[192 + key]));
+            const float old = first ? -INFINITY : mr[key];
+            const float now = (old == -INFINITY || m - old > p.tau) ? m : old;
+            al[key] = old == -INFINITY ? 1.f : fast_exp2(old - now);  // a row without keys so far has O = 0
+            mr[key] = now;
+            nm[key] = (now == -INFINITY ? 0.f : -now) + p.p_shift;
+          }
+          if (!meet()) return false;
+          if (!first) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (i < 16 * nch) l[i] *= al[i];
+            for (int c = 0; c < nch; ++c) {
+#pragma unroll
+              for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+                uint32_t w[16];
+                const uint32_t at = t_o + 16 * (term * nch + c);
+                tmem_ld_x16(at, w);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al[16 * c + i]);
+                tmem_st_x16(at, w);
+              }
+            }
+            tmem_st_wait();
+          }
+        }
+        first = false;
+        uint8_t* prow = smem + Lay::p_row(s, key);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c < nch) {
+            float e[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float4 n4 = reinterpret_cast<const float4*>(nm)[4 * c + q];
+              float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+              if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[4 * c + q];
+              const int i = 16 * c + 4 * q;
+              e[4 * q] = fast_exp2(fmaf(x[i], s4.x, n4.x));
+              e[4 * q + 1] = fast_exp2(fmaf(x[i + 1], s4.y, n4.y));
+              e[4 * q + 2] = fast_exp2(fmaf(x[i + 2], s4.z, n4.z));
+              e[4 * q + 3] = fast_exp2(fmaf(x[i + 3], s4.w, n4.w));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) l[16 * c + i] += e[i];
+            // 16-byte units of a key's row, permuted as the descriptors' 128-byte swizzle
+            if constexpr (F8) {
+              uint32_t hi[4], lo[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float h4[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) h4[k] = upper4(e[4 * i + k]);
+                hi[i] = pack_e4m3x2(h4[0], h4[1]) | (pack_e4m3x2(h4[2], h4[3]) << 16);
+                lo[i] = pack_e4m3x2(e[4 * i] - h4[0], e[4 * i + 1] - h4[1]) |
+                        (pack_e4m3x2(e[4 * i + 2] - h4[2], e[4 * i + 3] - h4[3]) << 16);
+              }
+              *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              *reinterpret_cast<uint4*>(prow + (((nch + c) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                *reinterpret_cast<uint4*>(prow + (((2 * c + k) ^ (key & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(e[8 * k], e[8 * k + 1]), pack_bf16x2(e[8 * k + 2], e[8 * k + 3]),
+                               pack_bf16x2(e[8 * k + 4], e[8 * k + 5]), pack_bf16x2(e[8 * k + 6], e[8 * k + 7]));
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::B_WPFULL + s));
+        ++w_pv;
+      }
+      // Row sums over the keys (lanes, then warps): a lane ends with row 32 b + lane.
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (32 * b < rows) {
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = l[32 * b + i];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (i < o) {
+                const bool up = (lane & o) != 0;
+                const float give = up ? v[i] : v[i + o], have = up ? v[i + o] : v[i];
+                v[i] = have + __shfl_xor_sync(0xffffffffu, give, o);
+              }
+            }
+          }
+          wm[wq * 64 + 32 * b + lane] = v[0];
+        }
+      }
+      if (first && key < 64) mr[key] = -INFINITY;  // no tile for this stream
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Lay::B_ML));
+      if (!wait(Lay::B_ML, m_phase, kSiteTMerge)) return false;
+      m_phase ^= 1u;
+      const bool whole = it.j0 == 0 && it.j1 == it.kvt;
+      const int64_t slot = static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0);
+      if (key < rows) {
+        // Both streams' state of row `key`; weights of their O, into nm and al of this stream.
+        const float* f = reinterpret_cast<const float*>(smem + Lay::SW_OFF);
+        float m2[2], l2[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float* g2 = f + i * Lay::SW_STREAM;
+          m2[i] = g2[128 + key];
+          l2[i] = (g2[192 + key] + g2[256 + key]) + (g2[320 + key] + g2[384 + key]);
+        }
+        const float m = fmaxf(m2[0], m2[1]);
+        const float w0 = m2[0] == -INFINITY ? 0.f : fast_exp2(m2[0] - m), w1 = m2[1] == -INFINITY ? 0.f : fast_exp2(m2[1] - m);
+        const float sum = l2[0] * w0 + l2[1] * w1;
+        const float f0 = whole ? (sum > 0.f ? 1.f / sum : 0.f) * p.o_scale : 1.f;
+        nm[key] = w0 * f0;
+        al[key] = w1 * f0;
+        if (s == 0) {
+          const int t2 = key / p.G, g2 = key - t2 * p.G;
+          if (whole)
+            p.lse[static_cast<int64_t>(it.h * p.G + g2) * p.T + it.q0 + it.tok0 + t2] =
+                sum > 0.f ? (m + __log2f(sum) - p.p_shift) * kLn2 : -INFINITY;
+          else
+            p.stat[slot * (2 * kBM) + key] = make_float2(m, sum);
+        }
+      }
+      if (!meet()) return false;
+      if (!wait(Lay::B_OFULL, o_phase, kSiteTOFull)) return false;
+      o_phase ^= 1u;
+      tc_fence_after();
+      // O^T: lane = dimension; this warpgroup takes every other group of 8 rows.
+      if (wq * 32 < D) {
+        const uint32_t t0 = tmem + lane_bits + Lay::TM_O0, t1 = tmem + lane_bits + Lay::TM_O1;
+        for (int c = s; 8 * c < rows; c += 2) {
+          float v[8];
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = 0.f;
+#pragma unroll
+          for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+            tmem_ld_x8(t0 + 8 * c + 16 * nch * term, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), nm[8 * c + i], v[i]);
+            if (nj > 1) {
+              tmem_ld_x8(t1 + 8 * c + 16 * nch * term, w);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), al[8 * c + i], v[i]);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = 8 * c + i;
+            if (row < rows) {
+              const int t2 = row / p.G, g2 = row - t2 * p.G;
+              if (whole)
+                p.o[(static_cast<int64_t>(it.q0 + it.tok0 + t2) * p.Hq + it.h * p.G + g2) * D + key] = __float2bfloat16(v[i]);
+              else
+                p.part[((slot * (D / 4) + (key >> 2)) * (2 * kBM) + row) * 4 + (key & 3)] = v[i];
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Lay::B_EPI));
+      if (!wait(Lay::B_EPI, e_phase, kSiteTMerge)) return false;
+      e_phase ^= 1u;
+      return true;
+    };
     bool ok = true;
     int4 hd = make_int4(-1, 0, 0, 0);  // the item whose first tiles this CTA holds without its last
     for (int x = x0; x < x1 && ok;) {
@@ -456,7 +797,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int mine_q = nq + (it.two ? s : 0);
         ok = wait(Lay::B_QFULL + (mine_q & 1), (mine_q >> 1) & 1, kSiteTQFull);
         if (!ok) break;
-        sl = p.scale_log2 * reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
+        sl = reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
+      }
+      if (it.swapped) {
+        ok = swapped_item(it, nq);
+        if (!ok) break;
+        ++nq;
+        finished();
+        continue;
       }
       nq += it.two ? 2 : 1;
       float m_ref = -INFINITY, l = 0.f;
@@ -688,6 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(Lay::B_EPI));
       ok = wait(Lay::B_EPI, e_phase, kSiteTMerge);
       e_phase ^= 1u;
+      finished();
     }
     if (threadIdx.x == 0) p.head[cta] = hd;
   } else {
@@ -702,16 +1051,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       const uint64_t pol = l2_policy_evict_normal();
-      uint32_t n_ld = 0;
-      int mine = -1;  // lane i: this warp's last copy into ring slot i
-      int nq = 0;
-      bool ok = true;
+      uint32_t n_ld = 0, issued = 0;  // tiles of earlier items, and tiles copied
+      int nq = 0, items = 0;
+      bool ok = true, was_swapped = false;
       const int per_tile = kBN / p.box_rows;  // copies of a full tile
       for (int x = x0; x < x1 && ok;) {
         const Seg it = list.at(x, x1);
         x = it.next;
         if (it.j0 >= it.j1) continue;
-        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
+        const int nj = it.j1 - it.j0;
         // The pages of 32 copies, one per lane, and of the next 32.
         const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
         auto pages_from = [&](int box) -> int {
@@ -720,37 +1068,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int win = pages_from(0), win_next = pages_from(32);
         const int tiles_per_win = 32 / per_tile;
-        if constexpr (!F8) {
+        if (!F8 && is_k) {
+          // A swapped item's P~ lies in the tiles of q: they are whole again when its products are done.
+          if (was_swapped && !it.swapped) ok = wait_items(items);
+          if (!ok) break;
           for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
-            if (!is_k) continue;
             const int slot = nq & 1;
             if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
             if (!ok) break;
             if (elect_one()) {
-              mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * p.tpt * p.G * Lay::ROWB);
+              const int tokens = it.swapped ? p.tpt64 : p.tpt;
+              mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * tokens * p.G * Lay::ROWB);
 #pragma unroll
               for (int c = 0; c < Lay::NCHUNK; ++c)
-                tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, &tm_q, bar(Lay::B_QFULL + slot),
-                            c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
+                tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, it.swapped ? &tm_q64 : &tm_q,
+                            bar(Lay::B_QFULL + slot), c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
             }
             __syncwarp();
           }
           if (!ok) break;
         }
+        was_swapped = it.swapped;
+        ++items;
         for (int j = 0; j < nj; ++j) {
           if (j > 0 && j % tiles_per_win == 0) {
             win = win_next;
             win_next = pages_from((j / tiles_per_win + 1) * 32);
           }
-          const uint32_t n = n_ld + (is_k ? k_pos(j, lead) : v_pos(j, nj, lead)), slot = n % NS;
-          if (n >= static_cast<uint32_t>(NS)) {
-            ok = wait(Lay::B_KVEMPTY + slot, ((n / NS) - 1) & 1u, kSiteTKvEmpty);
+          const uint32_t n = n_ld + j, slot = n % NR + (is_k ? 0 : NR);
+          if (n >= static_cast<uint32_t>(NR)) {
+            ok = wait(Lay::B_KVEMPTY + slot, ((n / NR) - 1) & 1u, kSiteTKvEmpty);
             if (!ok) break;
           }
+          issued = n + 1;
           const int kb = (it.j0 + j) * kBN;
           const int copies = min(per_tile, ceil_div(it.len - kb, p.box_rows));
           const int page = __shfl_sync(0xffffffffu, win, (j % tiles_per_win) * per_tile + (lane & (per_tile - 1)));
-          if (lane == static_cast<int>(slot)) mine = static_cast<int>(n);
           if (lane == 0) mbar_arrive_expect_tx(bar(Lay::B_KVFULL + slot), copies * p.box_rows * Lay::ROWB * Lay::NCHUNK);
           __syncwarp();
           if (lane < copies) {
@@ -765,15 +1118,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        n_ld += 2u * nj;
+        n_ld = issued;
       }
-      // This warp's copies have landed before the CTA may exit.  On an early end the other
-      // producer may have refilled a slot, which then runs out the limit.
-      for (int i = 0; i < NS; ++i) {
-        const int n = __shfl_sync(0xffffffffu, mine, i);
-        if (n >= 0 && (!ok || n + NS >= static_cast<int>(n_ld)))
-          drain_wait(bar(Lay::B_KVFULL + i), (n / NS) & 1, ok ? kDrainLimitNs : kDrainLimitNs / 8);
-      }
+      // This warp's copies have landed before the CTA may exit.
+      for (uint32_t n = issued > static_cast<uint32_t>(NR) ? issued - NR : 0u; n < issued; ++n)
+        drain_wait(bar(Lay::B_KVFULL + n % NR + (is_k ? 0 : NR)), (n / NR) & 1u, kDrainLimitNs);
       if (!F8 && is_k) {
         for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n) drain_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, kDrainLimitNs);
       }
@@ -784,13 +1133,110 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kHalf = kBN / 2;
       constexpr bool SW64 = Lay::ROWB == 64;
       uint32_t n_ld = 0, phases = 0, used = 0;  // bit b: phase of S buffer b, and whether it was used
-      int nq = 0;
-      bool ok = true;
+      uint32_t w_phase = 0, w_used = 0;         // the same for the streams of swapped items
+      int nq = 0, items = 0;
+      bool ok = true, was_swapped = false;
+      // Rows of a V tile from the sequence's end to the end of the last K step: whatever the
+      // page holds there must not meet the zero weights.
+      auto clear_rows = [&](uint32_t slot, int from, int to) {
+        if (from >= to) return;
+        constexpr int U = Lay::ROWB / 16;
+        const int units = (to - from) * U;
+        uint8_t* at = smem + Lay::KV_OFF + slot * Lay::TILE + from * Lay::ROWB;
+        for (int i = lane; i < units * Lay::NCHUNK; i += 32) {
+          const int c = i / units, w = i - c * units;
+          *reinterpret_cast<uint4*>(at + c * Lay::CHUNK + w * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
       for (int x = x0; x < x1 && ok;) {
         const Seg it = list.at(x, x1);
         x = it.next;
         if (it.j0 >= it.j1) continue;
-        const int nj = it.j1 - it.j0, lead = it.two ? 1 : 2;
+        const int nj = it.j1 - it.j0;
+        // TMEM changes hands between swapped and other items when the products are done.
+        if (warp == 9 && items > 0 && was_swapped != it.swapped) ok = wait_items(items);
+        if (!ok) break;
+        was_swapped = it.swapped;
+        ++items;
+        if (it.swapped) {
+          // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up to
+          // 16, twice with split operands (hi, then lo).  d = 64: V's 64 rows twice (LBO 0).
+          const uint32_t N = static_cast<uint32_t>((it.nt * p.G + 15) & ~15) * (F8 ? 2 : 1);
+          if (warp == 9) {
+            const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 0, 0) : idesc_bf16_f32(kBM, 0, 0, 0)) | ((N >> 3) << 17);
+            auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
+            ok = wait(Lay::B_QFULL + (nq & 1), (nq >> 1) & 1, kSiteTQFull);
+            const uint64_t dq = desc(sb + Lay::Q_OFF + (nq & 1) * Lay::QTILE);
+            for (int j = 0; j < nj && ok; ++j) {
+              const int s = j & 1;
+              const uint32_t n = n_ld + j, slot = n % NR;
+              ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
+              if (ok && ((w_used >> s) & 1u)) {  // the stream has read its last scores
+                ok = wait(Lay::B_WSFREE + s, (w_phase >> s) & 1u, kSiteTSFree);
+                w_phase ^= 1u << s;
+              }
+              if (!ok) break;
+              w_used |= 1u << s;
+              tc_fence_after();
+              const uint64_t dk = desc(sb + Lay::KV_OFF + slot * Lay::TILE);
+              const uint32_t tS = tmem + Lay::TM_S + 128 * s;
+              if (elect_one()) {
+                constexpr int PER = Lay::ROWB / 32;
+#pragma unroll
+                for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
+                  const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
+                  if constexpr (F8) mma_ss_f8(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
+                  else mma_ss(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
+                }
+                tc_commit(bar(Lay::B_WSFULL + s));
+                tc_commit(bar(Lay::B_KVEMPTY + slot));
+                if (j == nj - 1) tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
+              }
+              __syncwarp();
+            }
+          } else {
+            const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 1, 1) : idesc_bf16_f32(kBM, 0, 1, 1)) | ((N >> 3) << 17);
+            constexpr int NK = kBN / Lay::KSTEP;
+            constexpr int LBO = D == 64 ? 0 : Lay::CHUNK;
+            for (int j = 0; j < nj && ok; ++j) {
+              const int s = j & 1;
+              const uint32_t n = n_ld + j, slot = NR + n % NR;
+              const int left = it.len - (it.j0 + j) * kBN;
+              const int steps = min(NK, ceil_div(left, Lay::KSTEP));
+              ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
+              if (!ok) break;
+              clear_rows(slot, left, steps * Lay::KSTEP);
+              ok = wait(Lay::B_WPFULL + s, (w_phase >> s) & 1u, kSiteTPFull);
+              if (!ok) break;
+              w_phase ^= 1u << s;
+              tc_fence_after();
+              const uint32_t tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
+              const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE;
+              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, LBO, 512) : sdesc_sw128(vbase, LBO, 1024);
+              const uint32_t more = j >= 2 ? 1u : 0u;
+              if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < NK; ++kk) {
+                  if (kk >= steps) continue;
+                  const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
+                  const uint64_t dp = sdesc_sw128(sb + Lay::p_row(s, kk * Lay::KSTEP), 16, 1024);
+                  if constexpr (F8) mma_ss_f8(tO, dv, dp, idesc, kk > 0 ? 1u : more);
+                  else mma_ss(tO, dv, dp, idesc, kk > 0 ? 1u : more);
+                }
+                tc_commit(bar(Lay::B_WPVDONE + s));
+                tc_commit(bar(Lay::B_KVEMPTY + slot));
+                if (j == nj - 1) tc_commit(bar(Lay::B_OFULL));
+              }
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          n_ld += nj;
+          ++nq;
+          continue;
+        }
         const int steps2 = unit_count(it) >> 2;  // pairs of tiles (one row tile) or tiles (two)
         auto halves = [&](int j) { return it.len - (it.j0 + j) * kBN > kHalf ? 2 : 1; };
         if (warp == 9) {
@@ -803,11 +1249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // The units of both streams for one half: one round of waits, then all their products.
           for (int v = 0; v < steps2 && ok; ++v) {
             const int ja = it.two ? v : 2 * v, jb = it.two ? v : 2 * v + 1;
-            const uint32_t na = n_ld + k_pos(ja, lead), nb = n_ld + k_pos(jb, lead);
-            const uint32_t sa = na % NS, sbl = nb % NS;
+            const uint32_t na = n_ld + ja, nb = n_ld + jb;
+            const uint32_t sa = na % NR, sbl = nb % NR;
             const int ha = halves(ja), hb = jb < nj ? halves(jb) : 0;
-            ok = wait(Lay::B_KVFULL + sa, (na / NS) & 1u, kSiteTKvFull);
-            if (ok && !it.two && hb) ok = wait(Lay::B_KVFULL + sbl, (nb / NS) & 1u, kSiteTKvFull);
+            ok = wait(Lay::B_KVFULL + sa, (na / NR) & 1u, kSiteTKvFull);
+            if (ok && !it.two && hb) ok = wait(Lay::B_KVFULL + sbl, (nb / NR) & 1u, kSiteTKvFull);
             for (int half = 0; half < ha && ok; ++half) {  // the second tile is no fuller than the first
               const bool b_too = half < hb;
               const int b0 = 2 * half, b1 = b0 + 1;
@@ -867,27 +1313,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int s = 0; s < 2; ++s) {
                 if (s == 1 && half >= hb) continue;
                 const int j = s ? jb : ja, buf = 2 * half + s;
-                const uint32_t n = n_ld + v_pos(j, nj, lead), slot = n % NS;
+                const uint32_t n = n_ld + j, slot = NR + n % NR;
                 const int left = it.len - (it.j0 + j) * kBN - half * kHalf;  // keys of the half inside the sequence, or more
                 const int steps = min(NK, ceil_div(left, Lay::KSTEP));
                 if (!it.two || s == 0) {
                   if (half == 0) {
-                    ok = wait(Lay::B_KVFULL + slot, (n / NS) & 1u, kSiteTKvFull);
+                    ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
                     if (!ok) break;
                   }
-                  if (left < steps * Lay::KSTEP) {
-                    // Rows behind the sequence's end that the last K step would multiply:
-                    // whatever the page holds there must not meet the zero weights.
-                    constexpr int U = Lay::ROWB / 16;
-                    const int rows = steps * Lay::KSTEP - left;
-                    uint8_t* at = smem + Lay::KV_OFF + slot * Lay::TILE + (half * kHalf + left) * Lay::ROWB;
-                    for (int i = lane; i < rows * U * Lay::NCHUNK; i += 32) {
-                      const int c = i / (rows * U), w = i - c * rows * U;
-                      *reinterpret_cast<uint4*>(at + c * Lay::CHUNK + w * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                  }
+                  clear_rows(slot, half * kHalf + left, half * kHalf + steps * Lay::KSTEP);
                 }
                 ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
                 if (!ok) break;
@@ -922,7 +1356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         }
-        n_ld += 2u * nj;
+        n_ld += nj;
         nq += it.two ? 2 : 1;
       }
       // Every product issued by this warp completes before TMEM is freed.
@@ -1004,7 +1438,7 @@ constexpr int kMaxSmem = 232448;
 constexpr int kMaxGrid = 160;  // CTAs the workspace has room for (148 SMs)
 
 template <int D, bool F8>
-cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
+cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
                      int rows, cudaStream_t st) {
   using Lay = Layout<D, F8>;
   auto kern = tree_kernel<D, F8>;
@@ -1020,7 +1454,7 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  kern<<<grid, kThreads, smem, st>>>(tq, tk, tv, p);
+  kern<<<grid, kThreads, smem, st>>>(tq, tq64, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1068,6 +1502,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   p.rows = c.layers * c.pages * c.page_size;
   p.box_rows = c.page_size < kBN ? c.page_size : kBN;
   p.tpt = kBM / p.G;
+  p.tpt64 = 64 / p.G;
   const bool f8 = c.e4m3 != 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
   p.o_scale = f8 ? c.v_scale : 1.f;
@@ -1093,7 +1528,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
   // {d, heads, rows} of K and V, one box per page (or 128 rows of it); q as {d, G, heads, T}.
   const int esz = f8 ? 1 : 2, elems = (c.d * esz < 128 ? c.d : 128 / esz);
-  CUtensorMap tq = {}, tk, tv;
+  CUtensorMap tq = {}, tq64 = {}, tk, tv;
   const uint64_t kvd[3] = {static_cast<uint64_t>(c.d), static_cast<uint64_t>(c.heads),
                            static_cast<uint64_t>(c.layers) * c.pages * c.page_size};
   const uint64_t kvs[2] = {static_cast<uint64_t>(c.d) * esz, static_cast<uint64_t>(c.heads) * c.d * esz};
@@ -1108,10 +1543,14 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
                             static_cast<uint64_t>(a.Hq) * c.d * 2};
     const uint32_t qb[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt)};
     ok = attn_internal::make_tensor_map(&tq, a.q, 2, 4, qd, qs, qb, 128);
+    if (ok && p.tpt64 > 0) {
+      const uint32_t q64[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt64)};
+      ok = attn_internal::make_tensor_map(&tq64, a.q, 2, 4, qd, qs, q64, 128);
+    }
   }
   if (!ok) return ATTN_ERR_CUDA;
-  if (c.d == 128) *cuda = f8 ? launch_t<128, true>(tq, tk, tv, p, grid, rows, st) : launch_t<128, false>(tq, tk, tv, p, grid, rows, st);
-  else *cuda = f8 ? launch_t<64, true>(tq, tk, tv, p, grid, rows, st) : launch_t<64, false>(tq, tk, tv, p, grid, rows, st);
+  if (c.d == 128) *cuda = f8 ? launch_t<128, true>(tq, tq64, tk, tv, p, grid, rows, st) : launch_t<128, false>(tq, tq64, tk, tv, p, grid, rows, st);
+  else *cuda = f8 ? launch_t<64, true>(tq, tq64, tk, tv, p, grid, rows, st) : launch_t<64, false>(tq, tq64, tk, tv, p, grid, rows, st);
   return ATTN_OK;
 }
 

@@ -217,6 +217,33 @@ def test_many_sequences():
     verify(c, q, cu, None, o, lse)
 
 
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("masked", [False, True])
+def test_many_tiles_and_mixed_rows(dtype, d, masked):
+    """Every SM takes dozens of key tiles of many items, whose rows fill from a part of a tile to
+    several, one kind behind another."""
+    r = random.Random(d)
+    ctx = [r.randint(0, 3000) for _ in range(40)]
+    drafted = [r.choice([1, 1, 3, 16, 17, 33, 64, 130]) for _ in ctx]
+    c = build(ctx, drafted, 8, d, 32, dtype, seed=11)
+    mask = tree_mask(drafted, 5) if masked else None
+    q, cu, o, lse = run(c, drafted, 32, mask)
+    verify(c, q, cu, mask, o, lse)
+    for _ in range(3):
+        o2, l2 = ea.tree_fwd(c, q, cu, mask=mask)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("dtype,d", KINDS)
+def test_long_batches_of_single_tokens(dtype, d):
+    r = random.Random(d)
+    ctx = [r.randint(500, 6000) for _ in range(48)]
+    drafted = [1] * 48
+    c = build(ctx, drafted, 8, d, 64, dtype, seed=12)
+    q, cu, o, lse = run(c, drafted, 16)
+    verify(c, q, cu, None, o, lse)
+
+
 def test_rows_outside_the_batch_stay():
     c = build([100, 30], [3, 2], 1, 128, 16)
     q = torch.randn(12, 2, 128, device="cuda").to(torch.bfloat16)
