@@ -36,6 +36,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "cache_ops.h"
@@ -227,6 +228,17 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
 __device__ __forceinline__ float upper4(float x) {
   const float t = __fmul_rn(x, 1048577.f);
   return __fsub_rn(t, __fsub_rn(t, x));
+}
+
+// Rows of a swapped item's products.
+__device__ __forceinline__ int swapped_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+// Maximum over the warp, by the integer order of floats (negative ones with their bits reversed).
+__device__ __forceinline__ float warp_max(float x) {
+  int i = __float_as_int(x);
+  i ^= (i >> 31) & 0x7fffffff;
+  i = __reduce_max_sync(0xffffffffu, i);
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
 // Bits [0, k) of word g of a 128-bit set of columns.
@@ -453,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
                                       : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
             };
-            uint8_t* lo_at = it.swapped ? base + at(r + (rows + 15) / 16 * 16) : base + Lay::TILE + at(r);
+            uint8_t* lo_at = it.swapped ? base + at(r + swapped_rows(rows)) : base + Lay::TILE + at(r);
             *reinterpret_cast<uint2*>(base + at(r)) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
           }
@@ -492,8 +504,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P~ (rows side by side) goes to shared memory as the second operand of O^T += V^T P~^T.  The
     // maximum of a row is over lanes and warps: it is taken for the stream's first tile, and again
     // only when some score exceeds its row's reference by more than tau (a vote of the four warps).
-    auto swapped_item = [&](const Seg& it, int nq_item) -> bool {
-      const int nj = it.j1 - it.j0, rows = it.nt * p.G, nch = (rows + 15) >> 4;
+    // Unrolled for 16, 32 or 64 rows: the code of a tile is run straight through, and fetching it
+    // costs more than computing it when rows that do not exist are jumped over.
+    auto swapped_item = [&](const Seg& it, int nq_item, auto blocks) -> bool {
+      constexpr int NCH = decltype(blocks)::value, N = 16 * NCH;
+      const int nj = it.j1 - it.j0, rows = it.nt * p.G;
       const int key = r;
       float* st = reinterpret_cast<float*>(smem + Lay::SW_OFF) + s * Lay::SW_STREAM;
       float *nm = st, *al = st + 64, *mr = st + 128, *wm = st + 192;
@@ -507,27 +522,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         w_wg ^= 1u;
         return good;
       };
-      float l[64];
+      float l[N];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) l[i] = 0.f;
+      for (int i = 0; i < N; ++i) l[i] = 0.f;
       bool first = true;
       for (int j = s; j < nj; j += 2) {
         if (!wait(Lay::B_WSFULL + s, w_s_phase, kSiteTSFull)) return false;
         w_s_phase ^= 1u;
         tc_fence_after();
-        float x[64];
+        float x[N];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < nch) {
-            uint32_t w[16];
-            tmem_ld_x16(t_s + 16 * c, w);
+        for (int c = 0; c < NCH; ++c) {
+          uint32_t w[16];
+          tmem_ld_x16(t_s + 16 * c, w);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(w[i]);
-            if constexpr (F8) {
-              tmem_ld_x16(t_s + 16 * (nch + c), w);
+          for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(w[i]);
+          if constexpr (F8) {
+            tmem_ld_x16(t_s + N + 16 * c, w);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) x[16 * c + i] += __uint_as_float(w[i]);
-            }
+            for (int i = 0; i < 16; ++i) x[16 * c + i] += __uint_as_float(w[i]);
           }
         }
         tc_fence_before();
@@ -557,23 +570,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           vis[0] &= see[0];
           vis[1] &= see[1];
         }
-        if (part || (rows & 15)) {
+        if (part || rows != N) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i < 16 * nch && !((vis[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
+          for (int i = 0; i < N; ++i)
+            if (!((vis[i >> 5] >> (i & 31)) & 1u)) x[i] = -INFINITY;
         }
         bool renew = first;
         if (!first) {
           float top = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (c < 4 * nch) {
-              const float4 n4 = reinterpret_cast<const float4*>(nm)[c];
-              float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-              if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[c];
-              top = fmax3(top, fmaf(x[4 * c], s4.x, n4.x), fmaf(x[4 * c + 1], s4.y, n4.y));
-              top = fmax3(top, fmaf(x[4 * c + 2], s4.z, n4.z), fmaf(x[4 * c + 3], s4.w, n4.w));
-            }
+          for (int c = 0; c < 4 * NCH; ++c) {
+            const float4 n4 = reinterpret_cast<const float4*>(nm)[c];
+            float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+            if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[c];
+            top = fmax3(top, fmaf(x[4 * c], s4.x, n4.x), fmaf(x[4 * c + 1], s4.y, n4.y));
+            top = fmax3(top, fmaf(x[4 * c + 2], s4.z, n4.z), fmaf(x[4 * c + 3], s4.w, n4.w));
           }
           const bool over = __any_sync(0xffffffffu, top > p.tau + p.p_shift);
           if (over && lane == 0) vote[votes & 3] = 1;
@@ -588,13 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (renew) {
           float keep[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (i < 16 * nch) {
-              float y = x[i] * (F8 ? qs[i] : p.scale_log2);
-#pragma unroll
-              for (int o = 16; o; o >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, o));
-              if (lane == (i & 31)) keep[i >> 5] = y;
-            }
+          for (int i = 0; i < N; ++i) {
+            const float y = warp_max(x[i] * (F8 ? qs[i] : p.scale_log2));
+            if (lane == (i & 31)) keep[i >> 5] = y;
           }
           wm[wq * 64 + lane] = keep[0];
           wm[wq * 64 + 32 + lane] = keep[1];
@@ -610,13 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!meet()) return false;
           if (!first) {
 #pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (i < 16 * nch) l[i] *= al[i];
-            for (int c = 0; c < nch; ++c) {
+            for (int i = 0; i < N; ++i) l[i] *= al[i];
+#pragma unroll 1
+            for (int c = 0; c < NCH; ++c) {
 #pragma unroll
               for (int term = 0; term < (F8 ? 2 : 1); ++term) {
                 uint32_t w[16];
-                const uint32_t at = t_o + 16 * (term * nch + c);
+                const uint32_t at = t_o + N * term + 16 * c;
                 tmem_ld_x16(at, w);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * al[16 * c + i]);
@@ -629,8 +636,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = false;
         uint8_t* prow = smem + Lay::p_row(s, key);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c < nch) {
+        for (int c = 0; c < NCH; ++c) {
+          {
             float e[16];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -658,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         (pack_e4m3x2(e[4 * i + 2] - h4[2], e[4 * i + 3] - h4[3]) << 16);
               }
               *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(prow + (((nch + c) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              *reinterpret_cast<uint4*>(prow + (((NCH + c) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             } else {
 #pragma unroll
               for (int k = 0; k < 2; ++k)
@@ -676,11 +683,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // Row sums over the keys (lanes, then warps): a lane ends with row 32 b + lane.
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (32 * b < rows) {
+      for (int b = 0; b < (N + 31) / 32; ++b) {
+        {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = l[32 * b + i];
+          for (int i = 0; i < 32; ++i) v[i] = 32 * b + i < N ? l[32 * b + i < N ? 32 * b + i : 0] : 0.f;
 #pragma unroll
           for (int o = 16; o; o >>= 1) {
 #pragma unroll
@@ -741,11 +748,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 8; ++i) v[i] = 0.f;
 #pragma unroll
           for (int term = 0; term < (F8 ? 2 : 1); ++term) {
-            tmem_ld_x8(t0 + 8 * c + 16 * nch * term, w);
+            tmem_ld_x8(t0 + 8 * c + N * term, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), nm[8 * c + i], v[i]);
             if (nj > 1) {
-              tmem_ld_x8(t1 + 8 * c + 16 * nch * term, w);
+              tmem_ld_x8(t1 + 8 * c + N * term, w);
 #pragma unroll
               for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), al[8 * c + i], v[i]);
             }
@@ -800,7 +807,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         sl = reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
       }
       if (it.swapped) {
-        ok = swapped_item(it, nq);
+        const int width = swapped_rows(it.nt * p.G);
+        ok = width == 16   ? swapped_item(it, nq, std::integral_constant<int, 1>{})
+             : width == 32 ? swapped_item(it, nq, std::integral_constant<int, 2>{})
+                           : swapped_item(it, nq, std::integral_constant<int, 4>{});
         if (!ok) break;
         ++nq;
         finished();
@@ -1161,9 +1171,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         was_swapped = it.swapped;
         ++items;
         if (it.swapped) {
-          // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up to
-          // 16, twice with split operands (hi, then lo).  d = 64: V's 64 rows twice (LBO 0).
-          const uint32_t N = static_cast<uint32_t>((it.nt * p.G + 15) & ~15) * (F8 ? 2 : 1);
+          // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up,
+          // twice with split operands (hi, then lo).  d = 64: V's 64 rows twice (LBO 0).
+          const uint32_t N = static_cast<uint32_t>(swapped_rows(it.nt * p.G)) * (F8 ? 2 : 1);
           if (warp == 9) {
             const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 0, 0) : idesc_bf16_f32(kBM, 0, 0, 0)) | ((N >> 3) << 17);
             auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
@@ -1507,10 +1517,10 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
   p.o_scale = f8 ? c.v_scale : 1.f;
   // P~ <= 2^tau; on the E4M3 path it carries 2^p_shift, so that at most 256 of E4M3's 448 is
-  // reached and small weights stay normal numbers.  A low tau leaves room for the shift; its
-  // rescales are rare once the maximum has settled.
-  p.tau = f8 ? 2.f : 8.f;
-  p.p_shift = f8 ? 6.f : 0.f;
+  // reached.  tau 4 rather than 2: a maximum of 64 rows grew by 2 in most tiles (a rescale
+  // each), by 4 in few; small weights still keep 2^-9 absolute of the row's reference 2^4.
+  p.tau = f8 ? 4.f : 8.f;
+  p.p_shift = f8 ? 4.f : 0.f;
   p.err = a.err;
   char* ws = static_cast<char*>(a.ws);
   p.part = reinterpret_cast<float*>(ws);
