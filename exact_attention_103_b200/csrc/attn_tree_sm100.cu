@@ -115,9 +115,9 @@ struct Layout {
                        B_KVFULL = 31, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int TABLE_OFF = MISC_OFF + 128;
-  // Cost of a key tile with one and with two row tiles: the copies bound the first, the softmax
-  // of 256 rows the second.
-  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 1, COST_PAIR = ESZ * D == 256 ? 4 : 2;
+  // Cost of a key tile with one and with two row tiles (the copies bound the first, the softmax of
+  // 256 rows the second), and of beginning an item.
+  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 2, COST_PAIR = ESZ * D == 256 ? 4 : 4, COST_ITEM = 5;
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -141,13 +141,13 @@ struct Seg {
 };
 
 // The list of work, decoded alike by every role: items (sequence, cache head, row pair) one
-// behind the other, each key tile as long as its cost (`one` or `two` row tiles).  A tile
-// belongs to the CTA whose part holds its first unit; parts are no shorter than the longest
-// tile, so a part inside an item holds one of its tiles.  Tables in shared memory, per
-// sequence: cum (cost before it), first row of q, slot, tokens in the cache.
+// behind the other: the cost of beginning it, then each key tile as long as its cost (`one` or
+// `pair` of row tiles).  A tile belongs to the CTA whose part holds its first unit; parts are no
+// shorter than the longest tile, so a part among an item's tiles holds one of them.  Tables in
+// shared memory, per sequence: cum (cost before it), first row of q, slot, tokens in the cache.
 struct List {
   const int *cum, *cu, *slot, *len;
-  int B, heads, G, tpt, one, pair;
+  int B, heads, G, tpt, one, pair, item;
   bool masked;
 
   // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
@@ -174,8 +174,8 @@ struct List {
     s.h = r / per_head;
     r -= s.h * per_head;
     int rt = 0, kv = tiles(s.n, s.len, 0), w = cost(s.n, 0);
-    while (r >= kv * w) {
-      r -= kv * w;
+    while (r >= item + kv * w) {
+      r -= item + kv * w;
       ++rt;
       kv = tiles(s.n, s.len, rt);
       w = cost(s.n, rt);
@@ -186,9 +186,9 @@ struct List {
     s.swapped = s.nt * G <= 64;
     s.kvt = kv;
     s.begin = x - r;
-    s.next = min(end, s.begin + kv * w);
-    s.j0 = ceil_div(r, w);
-    s.j1 = ceil_div(s.next - s.begin, w);
+    s.next = min(end, s.begin + item + kv * w);
+    s.j0 = ceil_div(max(0, r - item), w);
+    s.j1 = ceil_div(max(0, s.next - s.begin - item), w);
     return s;
   }
 };
@@ -221,13 +221,6 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
     if (global_timer_ns() - t0 > limit_ns) return false;
   }
   return true;
-}
-
-// x rounded to 4 significant bits (Veltkamp's splitting: t = (2^20 + 1) x, t - (t - x)), in
-// roundings that must not be contracted to an fma.
-__device__ __forceinline__ float upper4(float x) {
-  const float t = __fmul_rn(x, 1048577.f);
-  return __fsub_rn(t, __fsub_rn(t, x));
 }
 
 // Rows of a swapped item's products.
@@ -309,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   list.tpt = p.tpt;
   list.one = Lay::COST_ONE;
   list.pair = Lay::COST_PAIR;
+  list.item = Lay::COST_ITEM;
   list.masked = p.mask != nullptr;
   {
     // The tiles of each sequence and their prefix sum; a thread takes consecutive sequences.
@@ -333,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) {
           record_invalid(p.err, bad);
         } else {
-          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.tiles(n, len, rt) * list.cost(n, rt);
+          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.item + list.tiles(n, len, rt) * list.cost(n, rt);
           work *= p.heads;
         }
       }
@@ -451,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int z = 0; z < 2; ++z) {
               const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
-              const float ha = upper4(a), hb = upper4(b);
+              float ha, hb;
+              upper4_x2(ha, hb, a, b);
               hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
               lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
             }
@@ -540,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (F8) {
             tmem_ld_x16(t_s + N + 16 * c, w);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[16 * c + i] += __uint_as_float(w[i]);
+            for (int i = 0; i < 16; i += 2)
+              fadd2_acc(x[16 * c + i], x[16 * c + i + 1], __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
           }
         }
         tc_fence_before();
@@ -570,6 +566,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           vis[0] &= see[0];
           vis[1] &= see[1];
         }
+        // x = scale s - reference (log2 units, times 2^p_shift); the first tile has no reference yet
+#pragma unroll
+        for (int c = 0; c < 4 * NCH; ++c) {
+          const float4 n4 = first ? make_float4(0.f, 0.f, 0.f, 0.f) : reinterpret_cast<const float4*>(nm)[c];
+          if constexpr (F8) {
+            const float4 s4 = reinterpret_cast<const float4*>(qs)[c];
+            ffma2_vv(x[4 * c], x[4 * c + 1], x[4 * c], x[4 * c + 1], s4.x, s4.y, n4.x, n4.y);
+            ffma2_vv(x[4 * c + 2], x[4 * c + 3], x[4 * c + 2], x[4 * c + 3], s4.z, s4.w, n4.z, n4.w);
+          } else {
+            ffma2_bv(x[4 * c], x[4 * c + 1], x[4 * c], x[4 * c + 1], p.scale_log2, n4.x, n4.y);
+            ffma2_bv(x[4 * c + 2], x[4 * c + 3], x[4 * c + 2], x[4 * c + 3], p.scale_log2, n4.z, n4.w);
+          }
+        }
         if (part || rows != N) {
 #pragma unroll
           for (int i = 0; i < N; ++i)
@@ -577,15 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bool renew = first;
         if (!first) {
-          float top = -INFINITY;
+          float top = x[0];
 #pragma unroll
-          for (int c = 0; c < 4 * NCH; ++c) {
-            const float4 n4 = reinterpret_cast<const float4*>(nm)[c];
-            float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-            if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[c];
-            top = fmax3(top, fmaf(x[4 * c], s4.x, n4.x), fmaf(x[4 * c + 1], s4.y, n4.y));
-            top = fmax3(top, fmaf(x[4 * c + 2], s4.z, n4.z), fmaf(x[4 * c + 3], s4.w, n4.w));
-          }
+          for (int i = 1; i + 1 < N; i += 2) top = fmax3(top, x[i], x[i + 1]);
+          top = fmaxf(top, x[N - 1]);
           const bool over = __any_sync(0xffffffffu, top > p.tau + p.p_shift);
           if (over && lane == 0) vote[votes & 3] = 1;
           if (!meet()) return false;
@@ -600,21 +604,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           float keep[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const float y = warp_max(x[i] * (F8 ? qs[i] : p.scale_log2));
+            const float y = warp_max(x[i]);  // relative to the reference so far
             if (lane == (i & 31)) keep[i >> 5] = y;
           }
           wm[wq * 64 + lane] = keep[0];
           wm[wq * 64 + 32 + lane] = keep[1];
           if (!meet()) return false;
           if (key < 64) {
-            const float m = fmaxf(fmaxf(wm[key], wm[64 + key]), fmaxf(wm[128 + key], wm[192 + key]));
-            const float old = first ? -INFINITY : mr[key];
+            // the tile's maximum relative to nm, the row's reference and its new one
+            const float rel = fmaxf(fmaxf(wm[key], wm[64 + key]), fmaxf(wm[128 + key], wm[192 + key]));
+            const float was = first ? 0.f : nm[key], old = first ? -INFINITY : mr[key];
+            const float m = rel - was;
             const float now = (old == -INFINITY || m - old > p.tau) ? m : old;
+            const float next = (now == -INFINITY ? 0.f : -now) + p.p_shift;
             al[key] = old == -INFINITY ? 1.f : fast_exp2(old - now);  // a row without keys so far has O = 0
             mr[key] = now;
-            nm[key] = (now == -INFINITY ? 0.f : -now) + p.p_shift;
+            nm[key] = next;
+            wm[key] = next - was;  // what the scores move by (the other warps' maxima have been read)
           }
           if (!meet()) return false;
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] += wm[i];
           if (!first) {
 #pragma unroll
             for (int i = 0; i < N; ++i) l[i] *= al[i];
@@ -640,29 +650,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           {
             float e[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const float4 n4 = reinterpret_cast<const float4*>(nm)[4 * c + q];
-              float4 s4 = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
-              if constexpr (F8) s4 = reinterpret_cast<const float4*>(qs)[4 * c + q];
-              const int i = 16 * c + 4 * q;
-              e[4 * q] = fast_exp2(fmaf(x[i], s4.x, n4.x));
-              e[4 * q + 1] = fast_exp2(fmaf(x[i + 1], s4.y, n4.y));
-              e[4 * q + 2] = fast_exp2(fmaf(x[i + 2], s4.z, n4.z));
-              e[4 * q + 3] = fast_exp2(fmaf(x[i + 3], s4.w, n4.w));
+            for (int i = 0; i < 16; i += 2) {
+              e[i] = fast_exp2(x[16 * c + i]);
+              e[i + 1] = fast_exp2(x[16 * c + i + 1]);
+              fadd2_acc(l[16 * c + i], l[16 * c + i + 1], e[i], e[i + 1]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) l[16 * c + i] += e[i];
             // 16-byte units of a key's row, permuted as the descriptors' 128-byte swizzle
             if constexpr (F8) {
               uint32_t hi[4], lo[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                float h4[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) h4[k] = upper4(e[4 * i + k]);
+                float h4[4], l4[4];
+                upper4_x2(h4[0], h4[1], e[4 * i], e[4 * i + 1]);
+                upper4_x2(h4[2], h4[3], e[4 * i + 2], e[4 * i + 3]);
+                fsub2(l4[0], l4[1], e[4 * i], e[4 * i + 1], h4[0], h4[1]);
+                fsub2(l4[2], l4[3], e[4 * i + 2], e[4 * i + 3], h4[2], h4[3]);
                 hi[i] = pack_e4m3x2(h4[0], h4[1]) | (pack_e4m3x2(h4[2], h4[3]) << 16);
-                lo[i] = pack_e4m3x2(e[4 * i] - h4[0], e[4 * i + 1] - h4[1]) |
-                        (pack_e4m3x2(e[4 * i + 2] - h4[2], e[4 * i + 3] - h4[3]) << 16);
+                lo[i] = pack_e4m3x2(l4[0], l4[1]) | (pack_e4m3x2(l4[2], l4[3]) << 16);
               }
               *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
               *reinterpret_cast<uint4*>(prow + (((NCH + c) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -785,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.j0 >= it.j1) continue;
       if (it.j0 == 0 && it.j1 < it.kvt) {
         // the CTA whose part holds the first unit of the item's last tile
-        const int64_t end = it.begin + (it.kvt - 1) * (it.two ? list.pair : list.one);
+        const int64_t end = it.begin + list.item + (it.kvt - 1) * (it.two ? list.pair : list.one);
         int last = static_cast<int>(end * ctas / total);
         while (static_cast<int64_t>(last + 1) * total / ctas <= end) ++last;
         while (static_cast<int64_t>(last) * total / ctas > end) --last;
@@ -930,8 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) {
             float a, e;
             exps(c, a, e);
-            const float ha = upper4(a), he = upper4(e);
-            const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(a - ha, e - he);
+            float ha, he, la, le;
+            upper4_x2(ha, he, a, e);
+            fsub2(la, le, a, e, ha, he);
+            const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(la, le);
             if (c & 1) {
               hi[c >> 1] |= wh << 16;
               lo[c >> 1] |= wl << 16;
@@ -1532,7 +1538,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   // describe.
   const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
   const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
-  if (items > INT32_MAX / (4 * tiles)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
+  if (items > INT32_MAX / (4 * tiles + 5)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
   int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
   if (grid > kMaxGrid) grid = kMaxGrid;
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;

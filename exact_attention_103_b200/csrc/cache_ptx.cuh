@@ -27,6 +27,25 @@ __device__ __forceinline__ uint64_t sdesc_sw64(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
+// Packed fp32 arithmetic with every operand per element: y = x * a + b.
+__device__ __forceinline__ void ffma2_vv(float& y0, float& y1, float x0, float x1, float a0, float a1, float b0,
+                                         float b1) {
+  asm("{\n\t.reg .b64 xa, aa, ba, ya;\n\t"
+      "mov.b64 xa, {%2, %3};\n\tmov.b64 aa, {%4, %5};\n\tmov.b64 ba, {%6, %7};\n\t"
+      "fma.rn.f32x2 ya, xa, aa, ba;\n\tmov.b64 {%0, %1}, ya;\n\t}"
+      : "=f"(y0), "=f"(y1)
+      : "f"(x0), "f"(x1), "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Two values rounded to 4 significant bits (Veltkamp's splitting: t = (2^20 + 1) x, t - (t - x)).
+// t is one fma, 2^20 x + x: a product would be contracted with the subtraction behind it.
+__device__ __forceinline__ void upper4_x2(float& h0, float& h1, float x0, float x1) {
+  float t0, t1, u0, u1;
+  ffma2_bv(t0, t1, x0, x1, 1048576.f, x0, x1);
+  fsub2(u0, u1, t0, t1, x0, x1);
+  fsub2(h0, h1, t0, t1, u0, u1);
+}
+
 // 16 columns of this warp's 32 lanes, complete on return (as tmem_ld_x8 and its wider forms).
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
