@@ -234,6 +234,17 @@ __device__ __forceinline__ float warp_max(float x) {
   return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
+// The scores of a swapped item's key: N columns in one load.
+template <int N>
+__device__ __forceinline__ void load_scores(uint32_t at, float (&x)[N]) {
+  uint32_t w[N];
+  if constexpr (N == 64) tmem_ld_x64(at, w);
+  else if constexpr (N == 32) tmem_ld_x32(at, w);
+  else tmem_ld_x16(at, w);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(w[i]);
+}
+
 // Bits [0, k) of word g of a 128-bit set of columns.
 __device__ __forceinline__ uint32_t below(int k, int g) {
   k -= 32 * g;
@@ -473,6 +484,94 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // Producers: K (and q) by one warp, V by another.
+  auto produce = [&](auto keys) {
+    constexpr bool is_k = decltype(keys)::value;
+    if (elect_one()) {
+      if (is_k && !F8) tma_prefetch_map(&tm_q);
+      tma_prefetch_map(is_k ? &tm_k : &tm_v);
+    }
+    __syncwarp();
+    const uint64_t pol = l2_policy_evict_normal();
+    uint32_t n = 0;  // tiles copied
+    int nq = 0, items = 0;
+    bool ok = true, was_swapped = false;
+    // A tile is copied in boxes of box_rows keys, box i by lane i; per_tile is a power of two.
+    const int per_tile = kBN / p.box_rows;
+    const int box_bytes = p.box_rows * Lay::ROWB * Lay::NCHUNK;
+    const uint32_t lane_dst = sb + Lay::KV_OFF + (is_k ? 0 : NR * Lay::TILE) + lane * p.box_rows * Lay::ROWB;
+    const int in_page = (1 << p.page_shift) - 1;
+    for (int x = x0; x < x1 && ok;) {
+      const Seg it = list.at(x, x1);
+      x = it.next;
+      if (it.j0 >= it.j1) continue;
+      // The pages of 32 boxes, one per lane, and of the next 32.
+      const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
+      const int first = it.j0 * kBN, end = min(it.len, it.j1 * kBN);
+      auto pages_from = [&](int pos) -> int {
+        pos += lane * p.box_rows;
+        return pos < end ? __ldg(row + (pos >> p.page_shift)) : 0;
+      };
+      int win = 0, win_next = pages_from(first), from = 32;  // from: the next box's lane in win
+      int pos = first, next_win = first;
+      if (!F8 && is_k) {
+        // A swapped item's P~ lies in the tiles of q: they are whole again when its products are done.
+        if (was_swapped && !it.swapped) ok = wait_items(items);
+        for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
+          const int slot = nq & 1;
+          if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
+          if (!ok) break;
+          if (elect_one()) {
+            const int tokens = it.swapped ? p.tpt64 : p.tpt;
+            mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * tokens * p.G * Lay::ROWB);
+#pragma unroll
+            for (int c = 0; c < Lay::NCHUNK; ++c)
+              tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, it.swapped ? &tm_q64 : &tm_q,
+                          bar(Lay::B_QFULL + slot), c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      was_swapped = it.swapped;
+      ++items;
+      for (int j = it.j0; j < it.j1; ++j, ++n, pos += kBN, from += per_tile) {
+        if (from == 32) {
+          from = 0;
+          win = win_next;
+          next_win += 32 * p.box_rows;
+          win_next = pages_from(next_win);
+        }
+        const uint32_t slot = n % NR, full = bar(Lay::B_KVFULL + (is_k ? 0 : NR)) + 8 * slot;
+        const int page = __shfl_sync(0xffffffffu, win, from + (lane & (per_tile - 1)));
+        const int mine = pos + lane * p.box_rows;
+        const bool copies = lane < per_tile && mine < it.len;
+        int at = p.rows;
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pages)) at = p.layer_row + (page << p.page_shift) + (mine & in_page);
+        else if (copies) record_invalid(p.err, kSitePage);
+        const int boxes = min(per_tile, (it.len - pos + p.box_rows - 1) / p.box_rows);
+        if (n >= static_cast<uint32_t>(NR)) {
+          ok = wait(Lay::B_KVEMPTY + (is_k ? 0 : NR) + slot, ((n / NR) - 1) & 1u, kSiteTKvEmpty);
+          if (!ok) break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full, boxes * box_bytes);
+        __syncwarp();
+        if (copies) {
+#pragma unroll
+          for (int c = 0; c < Lay::NCHUNK; ++c)
+            tma_load_3d(lane_dst + slot * Lay::TILE + c * Lay::CHUNK, is_k ? &tm_k : &tm_v, full, c * Lay::CELEMS, it.h, at, pol);
+        }
+        __syncwarp();
+      }
+    }
+    // This warp's copies have landed before the CTA may exit.
+    for (uint32_t i = n > static_cast<uint32_t>(NR) ? n - NR : 0u; i < n; ++i)
+      drain_wait(bar(Lay::B_KVFULL + i % NR + (is_k ? 0 : NR)), (i / NR) & 1u, kDrainLimitNs);
+    if (!F8 && is_k) {
+      for (int i = nq > 2 ? nq - 2 : 0; i < nq; ++i) drain_wait(bar(Lay::B_QFULL + (i & 1)), (i >> 1) & 1, kDrainLimitNs);
+    }
+  };
+
   // 4 x 32 x (168 - 120) registers released by warpgroup 2, 8 x 32 x (192 - 168) taken.
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n" ::: "memory");
@@ -526,19 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w_s_phase ^= 1u;
         tc_fence_after();
         float x[N];
-#pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-          uint32_t w[16];
-          tmem_ld_x16(t_s + 16 * c, w);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[16 * c + i] = __uint_as_float(w[i]);
-          if constexpr (F8) {
-            tmem_ld_x16(t_s + N + 16 * c, w);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              fadd2_acc(x[16 * c + i], x[16 * c + i + 1], __uint_as_float(w[i]), __uint_as_float(w[i + 1]));
-          }
-        }
+        load_scores(t_s, x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Lay::B_WSFREE + s));
@@ -1057,91 +1144,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) p.head[cta] = hd;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n" ::: "memory");
-    if (warp == 8 || warp == 10) {
-      // --------------------------------------------------- producers: K (and q), V
-      const bool is_k = warp == 8;
-      const CUtensorMap* map = is_k ? &tm_k : &tm_v;
-      if (elect_one()) {
-        if (is_k && !F8) tma_prefetch_map(&tm_q);
-        tma_prefetch_map(map);
-      }
-      __syncwarp();
-      const uint64_t pol = l2_policy_evict_normal();
-      uint32_t n_ld = 0, issued = 0;  // tiles of earlier items, and tiles copied
-      int nq = 0, items = 0;
-      bool ok = true, was_swapped = false;
-      const int per_tile = kBN / p.box_rows;  // copies of a full tile
-      for (int x = x0; x < x1 && ok;) {
-        const Seg it = list.at(x, x1);
-        x = it.next;
-        if (it.j0 >= it.j1) continue;
-        const int nj = it.j1 - it.j0;
-        // The pages of 32 copies, one per lane, and of the next 32.
-        const int32_t* row = p.page_table + static_cast<int64_t>(it.slot) * p.max_pages;
-        auto pages_from = [&](int box) -> int {
-          const int pos = it.j0 * kBN + (box + lane) * p.box_rows;
-          return (box < nj * per_tile && pos < it.len) ? __ldg(row + (pos >> p.page_shift)) : 0;
-        };
-        int win = pages_from(0), win_next = pages_from(32);
-        const int tiles_per_win = 32 / per_tile;
-        if (!F8 && is_k) {
-          // A swapped item's P~ lies in the tiles of q: they are whole again when its products are done.
-          if (was_swapped && !it.swapped) ok = wait_items(items);
-          if (!ok) break;
-          for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k, ++nq) {
-            const int slot = nq & 1;
-            if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
-            if (!ok) break;
-            if (elect_one()) {
-              const int tokens = it.swapped ? p.tpt64 : p.tpt;
-              mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * tokens * p.G * Lay::ROWB);
-#pragma unroll
-              for (int c = 0; c < Lay::NCHUNK; ++c)
-                tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, it.swapped ? &tm_q64 : &tm_q,
-                            bar(Lay::B_QFULL + slot), c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-        }
-        was_swapped = it.swapped;
-        ++items;
-        for (int j = 0; j < nj; ++j) {
-          if (j > 0 && j % tiles_per_win == 0) {
-            win = win_next;
-            win_next = pages_from((j / tiles_per_win + 1) * 32);
-          }
-          const uint32_t n = n_ld + j, slot = n % NR + (is_k ? 0 : NR);
-          if (n >= static_cast<uint32_t>(NR)) {
-            ok = wait(Lay::B_KVEMPTY + slot, ((n / NR) - 1) & 1u, kSiteTKvEmpty);
-            if (!ok) break;
-          }
-          issued = n + 1;
-          const int kb = (it.j0 + j) * kBN;
-          const int copies = min(per_tile, ceil_div(it.len - kb, p.box_rows));
-          const int page = __shfl_sync(0xffffffffu, win, (j % tiles_per_win) * per_tile + (lane & (per_tile - 1)));
-          if (lane == 0) mbar_arrive_expect_tx(bar(Lay::B_KVFULL + slot), copies * p.box_rows * Lay::ROWB * Lay::NCHUNK);
-          __syncwarp();
-          if (lane < copies) {
-            const int pos = kb + lane * p.box_rows;
-            int at = p.rows;
-            if (page >= 0 && page < p.pages) at = p.layer_row + (page << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
-            else record_invalid(p.err, kSitePage);
-            const uint32_t dst = sb + Lay::KV_OFF + slot * Lay::TILE + lane * p.box_rows * Lay::ROWB;
-#pragma unroll
-            for (int c = 0; c < Lay::NCHUNK; ++c)
-              tma_load_3d(dst + c * Lay::CHUNK, map, bar(Lay::B_KVFULL + slot), c * Lay::CELEMS, it.h, at, pol);
-          }
-          __syncwarp();
-        }
-        n_ld = issued;
-      }
-      // This warp's copies have landed before the CTA may exit.
-      for (uint32_t n = issued > static_cast<uint32_t>(NR) ? issued - NR : 0u; n < issued; ++n)
-        drain_wait(bar(Lay::B_KVFULL + n % NR + (is_k ? 0 : NR)), (n / NR) & 1u, kDrainLimitNs);
-      if (!F8 && is_k) {
-        for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n) drain_wait(bar(Lay::B_QFULL + (n & 1)), (n >> 1) & 1, kDrainLimitNs);
-      }
+    if (warp == 8) {
+      produce(std::true_type{});
+    } else if (warp == 10) {
+      produce(std::false_type{});
     } else {
       // ------------------------------------------------- products: S (9), P~V (11)
       // Two warps issue them, so that one's waits run beside the other's products: a lone
@@ -1177,11 +1183,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         was_swapped = it.swapped;
         ++items;
         if (it.swapped) {
-          // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up,
-          // twice with split operands (hi, then lo).  d = 64: V's 64 rows twice (LBO 0).
-          const uint32_t N = static_cast<uint32_t>(swapped_rows(it.nt * p.G)) * (F8 ? 2 : 1);
+          // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up.
+          // Split operands: S sums both terms; O has 2 N columns, hi's and lo's.  d = 64: V's 64 rows
+          // twice (LBO 0).
+          const uint32_t N = static_cast<uint32_t>(swapped_rows(it.nt * p.G));
           if (warp == 9) {
             const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 0, 0) : idesc_bf16_f32(kBM, 0, 0, 0)) | ((N >> 3) << 17);
+            const uint32_t lo = N * Lay::ROWB;  // the lo rows of split queries
             auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
             ok = wait(Lay::B_QFULL + (nq & 1), (nq >> 1) & 1, kSiteTQFull);
             const uint64_t dq = desc(sb + Lay::Q_OFF + (nq & 1) * Lay::QTILE);
@@ -1203,8 +1211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
                   const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
-                  if constexpr (F8) mma_ss_f8(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
-                  else mma_ss(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
+                  if constexpr (F8) {
+                    mma_ss_f8(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
+                    mma_ss_f8(tS, desc_add(dk, off), desc_add(dq, off + lo), idesc, 1u);
+                  } else {
+                    mma_ss(tS, desc_add(dk, off), desc_add(dq, off), idesc, kk > 0);
+                  }
                 }
                 tc_commit(bar(Lay::B_WSFULL + s));
                 tc_commit(bar(Lay::B_KVEMPTY + slot));
@@ -1213,7 +1225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
           } else {
-            const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 1, 1) : idesc_bf16_f32(kBM, 0, 1, 1)) | ((N >> 3) << 17);
+            const uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, 0, 1, 1) | ((N >> 2) << 17) : idesc_bf16_f32(kBM, 0, 1, 1) | ((N >> 3) << 17);
             constexpr int NK = kBN / Lay::KSTEP;
             constexpr int LBO = D == 64 ? 0 : Lay::CHUNK;
             for (int j = 0; j < nj && ok; ++j) {
