@@ -58,6 +58,8 @@ enum TreeSite : int {  // wait sites of the device error word (16..30)
 };
 __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
 
+constexpr int kMinPart = 4;  // no CTA takes less of the list: the longest tile
+
 struct TreeParams {
   __nv_bfloat16* o;
   float* lse;
@@ -117,7 +119,7 @@ struct Layout {
   static constexpr int TABLE_OFF = MISC_OFF + 128;
   // Cost of a key tile with one and with two row tiles (the copies bound the first, the softmax of
   // 256 rows the second), and of beginning an item.
-  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 2, COST_PAIR = ESZ * D == 256 ? 4 : 4, COST_ITEM = 5;
+  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 2, COST_PAIR = ESZ * D == 256 ? 4 : 4, COST_ITEM = ESZ * D == 256 ? 10 : 12;
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -302,6 +304,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(sb + Lay::MISC_OFF, 512);
     tmem_relinquish();
   }
+  // The page table's lines on their way while the list is built (as many as there are threads).
+  {
+    const int lines = (p.max_pages + 31) >> 5;
+    const int b = static_cast<int>(threadIdx.x) / lines;
+    if (b < p.B) {
+      const int slot = p.slots ? __ldg(p.slots + b) : b;
+      if (slot >= 0 && slot < p.nslots)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(p.page_table + static_cast<int64_t>(slot) * p.max_pages +
+                                                      32 * (static_cast<int>(threadIdx.x) - b * lines)));
+    }
+  }
   List list;
   list.cum = t_cum;
   list.cu = t_cu;
@@ -376,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = misc[0];
   const int total = t_cum[p.B];
   // CTAs with work; a part holds at least one tile
-  const int ctas = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / Lay::COST_PAIR)) : 0;
+  const int ctas = total > 0 ? max(1, min(static_cast<int>(gridDim.x), total / kMinPart)) : 0;
   const int cta = static_cast<int>(blockIdx.x);
   const int x0 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta) * total / ctas) : 0;
   const int x1 = cta < ctas ? static_cast<int>(static_cast<int64_t>(cta + 1) * total / ctas) : 0;
@@ -896,6 +909,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(Lay::B_QFULL + (mine_q & 1), (mine_q >> 1) & 1, kSiteTQFull);
         if (!ok) break;
         sl = reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
+      }
+      if (p.mask != nullptr && it.j1 * kBN > it.ctx) {
+        // The mask rows of this warp's tokens will be needed for the last tiles.
+        const int t0 = it.swapped ? 0 : (wq * 32) / p.G, t1 = it.swapped ? it.nt - 1 : min((wq * 32 + 31) / p.G, mine - 1);
+        const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first + t0) * p.mask_width;
+        for (int i = lane * 128; i < (t1 - t0 + 1) * p.mask_width; i += 32 * 128)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + i));
       }
       if (it.swapped) {
         const int width = swapped_rows(it.nt * p.G);
@@ -1550,7 +1570,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   // describe.
   const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
   const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
-  if (items > INT32_MAX / (4 * tiles + 5)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
+  if (items > INT32_MAX / (4 * tiles + 12)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
   int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
   if (grid > kMaxGrid) grid = kMaxGrid;
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
