@@ -58,6 +58,10 @@ enum TreeSite : int {  // wait sites of the device error word (16..30)
 };
 __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
 
+// Items of at most this many rows compute transposed scores.  Measured (8 sequences of 8192 tokens, 4
+// heads a cache head, bf16 / E4M3, us): 32 rows 65 / 58 transposed; 64 rows 80 / 81 transposed, 73 / 68
+// as one row tile, where every row has a thread and its reference stays in a register.
+constexpr int kSwapped = 32;
 constexpr int kMinPart = 4;  // no CTA takes less of the list: the longest tile
 
 struct TreeParams {
@@ -73,7 +77,7 @@ struct TreeParams {
   int rows;        // rows of the tensor maps: a copy from there on gives zeros
   int box_rows;    // rows of one K/V copy: min(page size, 128)
   int tpt;         // tokens of a 128-row tile: 128 / G
-  int tpt64;       // tokens of 64 rows: 64 / G
+  int tpt32;       // tokens of a swapped item's copy of q: kSwapped / G
   float scale_log2, o_scale, tau, p_shift;
   float* part;     // [grid][2][D / 4][256][4] unnormalised O: four columns of neighbouring rows
                    // lie together, as the lanes that write and join them are neighbouring rows
@@ -139,7 +143,7 @@ struct Seg {
   int j0, j1, kvt;
   int begin, next;        // where the item begins in the list, and the next stretch
   bool two;               // more than one row tile
-  bool swapped;           // at most 64 rows
+  bool swapped;           // at most kSwapped rows
 };
 
 // The list of work, decoded alike by every role: items (sequence, cache head, row pair) one
@@ -185,7 +189,7 @@ struct List {
     s.tok0 = rt * 2 * tpt;
     s.nt = min(2 * tpt, s.n - s.tok0);
     s.two = s.nt > tpt;
-    s.swapped = s.nt * G <= 64;
+    s.swapped = s.nt * G <= kSwapped;
     s.kvt = kv;
     s.begin = x - r;
     s.next = min(end, s.begin + item + kv * w);
@@ -226,7 +230,7 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
 }
 
 // Rows of a swapped item's products.
-__device__ __forceinline__ int swapped_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+__device__ __forceinline__ int swapped_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
 // Maximum over the warp, by the integer order of floats (negative ones with their bits reversed).
 __device__ __forceinline__ float warp_max(float x) {
@@ -240,8 +244,7 @@ __device__ __forceinline__ float warp_max(float x) {
 template <int N>
 __device__ __forceinline__ void load_scores(uint32_t at, float (&x)[N]) {
   uint32_t w[N];
-  if constexpr (N == 64) tmem_ld_x64(at, w);
-  else if constexpr (N == 32) tmem_ld_x32(at, w);
+  if constexpr (N == 32) tmem_ld_x32(at, w);
   else tmem_ld_x16(at, w);
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __uint_as_float(w[i]);
@@ -255,7 +258,7 @@ __device__ __forceinline__ uint32_t below(int k, int g) {
 
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads, 1)
-    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q64,
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q32,
                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ TreeParams p) {
   using Lay = Layout<D, F8>;
@@ -535,11 +538,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (nq >= 2) ok = wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty);
           if (!ok) break;
           if (elect_one()) {
-            const int tokens = it.swapped ? p.tpt64 : p.tpt;
+            const int tokens = it.swapped ? p.tpt32 : p.tpt;
             mbar_arrive_expect_tx(bar(Lay::B_QFULL + slot), Lay::NCHUNK * tokens * p.G * Lay::ROWB);
 #pragma unroll
             for (int c = 0; c < Lay::NCHUNK; ++c)
-              tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, it.swapped ? &tm_q64 : &tm_q,
+              tma_load_4d(sb + Lay::Q_OFF + slot * Lay::QTILE + c * Lay::CHUNK, it.swapped ? &tm_q32 : &tm_q,
                           bar(Lay::B_QFULL + slot), c * Lay::CELEMS, 0, it.h, it.q0 + it.tok0 + k * p.tpt, pol);
           }
           __syncwarp();
@@ -606,12 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sb + Lay::MISC_OFF + 8), "r"(items) : "memory");
     };
     uint32_t w_s_phase = 0, w_pv = 0, w_wg = 0, votes = 0;  // swapped items; w_pv: P~ handed over
-    // An item of at most 64 rows, scores transposed: a thread holds one key of the tile and all
+    // An item of few rows, scores transposed: a thread holds one key of the tile and all
     // rows, so all four warps of the stream share the exponentials, however few rows there are.
     // P~ (rows side by side) goes to shared memory as the second operand of O^T += V^T P~^T.  The
     // maximum of a row is over lanes and warps: it is taken for the stream's first tile, and again
     // only when some score exceeds its row's reference by more than tau (a vote of the four warps).
-    // Unrolled for 16, 32 or 64 rows: the code of a tile is run straight through, and fetching it
+    // Unrolled for 16 or 32 rows: the code of a tile is run straight through, and fetching it
     // costs more than computing it when rows that do not exist are jumped over.
     auto swapped_item = [&](const Seg& it, int nq_item, auto blocks) -> bool {
       constexpr int NCH = decltype(blocks)::value, N = 16 * NCH;
@@ -919,9 +922,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (it.swapped) {
         const int width = swapped_rows(it.nt * p.G);
-        ok = width == 16   ? swapped_item(it, nq, std::integral_constant<int, 1>{})
-             : width == 32 ? swapped_item(it, nq, std::integral_constant<int, 2>{})
-                           : swapped_item(it, nq, std::integral_constant<int, 4>{});
+        ok = width == 16 ? swapped_item(it, nq, std::integral_constant<int, 1>{})
+                         : swapped_item(it, nq, std::integral_constant<int, 2>{});
         if (!ok) break;
         ++nq;
         finished();
@@ -1486,7 +1488,7 @@ constexpr int kMaxSmem = 232448;
 constexpr int kMaxGrid = 160;  // CTAs the workspace has room for (148 SMs)
 
 template <int D, bool F8>
-cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq64, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
+cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq32, const CUtensorMap& tk, const CUtensorMap& tv, const TreeParams& p, int grid,
                      int rows, cudaStream_t st) {
   using Lay = Layout<D, F8>;
   auto kern = tree_kernel<D, F8>;
@@ -1502,7 +1504,7 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq64, const CUten
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  kern<<<grid, kThreads, smem, st>>>(tq, tq64, tk, tv, p);
+  kern<<<grid, kThreads, smem, st>>>(tq, tq32, tk, tv, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -1550,7 +1552,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   p.rows = c.layers * c.pages * c.page_size;
   p.box_rows = c.page_size < kBN ? c.page_size : kBN;
   p.tpt = kBM / p.G;
-  p.tpt64 = 64 / p.G;
+  p.tpt32 = kSwapped / p.G;
   const bool f8 = c.e4m3 != 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
   p.o_scale = f8 ? c.v_scale : 1.f;
@@ -1576,7 +1578,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
   // {d, heads, rows} of K and V, one box per page (or 128 rows of it); q as {d, G, heads, T}.
   const int esz = f8 ? 1 : 2, elems = (c.d * esz < 128 ? c.d : 128 / esz);
-  CUtensorMap tq = {}, tq64 = {}, tk, tv;
+  CUtensorMap tq = {}, tq32 = {}, tk, tv;
   const uint64_t kvd[3] = {static_cast<uint64_t>(c.d), static_cast<uint64_t>(c.heads),
                            static_cast<uint64_t>(c.layers) * c.pages * c.page_size};
   const uint64_t kvs[2] = {static_cast<uint64_t>(c.d) * esz, static_cast<uint64_t>(c.heads) * c.d * esz};
@@ -1591,14 +1593,14 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
                             static_cast<uint64_t>(a.Hq) * c.d * 2};
     const uint32_t qb[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt)};
     ok = attn_internal::make_tensor_map(&tq, a.q, 2, 4, qd, qs, qb, 128);
-    if (ok && p.tpt64 > 0) {
-      const uint32_t q64[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt64)};
-      ok = attn_internal::make_tensor_map(&tq64, a.q, 2, 4, qd, qs, q64, 128);
+    if (ok && p.tpt32 > 0) {
+      const uint32_t q32[4] = {64, static_cast<uint32_t>(p.G), 1, static_cast<uint32_t>(p.tpt32)};
+      ok = attn_internal::make_tensor_map(&tq32, a.q, 2, 4, qd, qs, q32, 128);
     }
   }
   if (!ok) return ATTN_ERR_CUDA;
-  if (c.d == 128) *cuda = f8 ? launch_t<128, true>(tq, tq64, tk, tv, p, grid, rows, st) : launch_t<128, false>(tq, tq64, tk, tv, p, grid, rows, st);
-  else *cuda = f8 ? launch_t<64, true>(tq, tq64, tk, tv, p, grid, rows, st) : launch_t<64, false>(tq, tq64, tk, tv, p, grid, rows, st);
+  if (c.d == 128) *cuda = f8 ? launch_t<128, true>(tq, tq32, tk, tv, p, grid, rows, st) : launch_t<128, false>(tq, tq32, tk, tv, p, grid, rows, st);
+  else *cuda = f8 ? launch_t<64, true>(tq, tq32, tk, tv, p, grid, rows, st) : launch_t<64, false>(tq, tq32, tk, tv, p, grid, rows, st);
   return ATTN_OK;
 }
 
