@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  let_next_launch();
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(Lay::B_QFULL + s), F8 ? 8 : 1);  // E4M3: written by the softmax warps
@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(sb + Lay::MISC_OFF, 512);
     tmem_relinquish();
   }
+  wait_for_previous();
   // The page table's lines on their way while the list is built (as many as there are threads).
   {
     const int lines = (p.max_pages + 31) >> 5;
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (slot < 0 || slot >= p.nslots) {
           bad = kSiteSlot;
         } else {
-          len = __ldg(p.lens + slot);
+          len = __ldcg(p.lens + slot);
           if (len < n || len > (static_cast<int64_t>(p.max_pages) << p.page_shift) || (p.mask && n > p.mask_width))
             bad = kSiteLength;
         }
@@ -444,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < U; ++i) {
           const int r = r0 + 8 * R * i, t = r / p.G, gg = r - t * p.G;
           w[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows) w[i] = __ldg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
+          if (r < rows) w[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
@@ -526,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int first = it.j0 * kBN, end = min(it.len, it.j1 * kBN);
       auto pages_from = [&](int pos) -> int {
         pos += lane * p.box_rows;
-        return pos < end ? __ldg(row + (pos >> p.page_shift)) : 0;
+        return pos < end ? __ldcg(row + (pos >> p.page_shift)) : 0;
       };
       int win = 0, win_next = pages_from(first), from = 32;  // from: the next box's lane in win
       int pos = first, next_win = first;
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* st = reinterpret_cast<float*>(smem + Lay::SW_OFF) + s * Lay::SW_STREAM;
       float *nm = st, *al = st + 64, *mr = st + 128, *wm = st + 192;
       volatile int* vote = reinterpret_cast<volatile int*>(st + 448);
-      const float* qs = reinterpret_cast<const float*>(smem + Lay::QS_OFF) + (nq_item & 1) * kBM;
+      [[maybe_unused]] const float* qs = reinterpret_cast<const float*>(smem + Lay::QS_OFF) + (nq_item & 1) * kBM;
       const uint32_t t_s = tmem + lane_bits + Lay::TM_S + 128 * s;
       auto meet = [&]() -> bool {  // the stream's four warps
         __syncwarp();
@@ -1429,7 +1430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // columns of a row, eight parts at a time.
 template <int D>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ TreeParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  let_next_launch();
+  wait_for_previous();
   const int c = blockIdx.x;
   const int4 hd = p.head[c];
   if (hd.x < 0) return;
@@ -1504,19 +1506,9 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq32, const CUten
     if (e != cudaSuccess) return e;
     ready.fetch_or(1ull << dev, std::memory_order_release);
   }
-  kern<<<grid, kThreads, smem, st>>>(tq, tq32, tk, tv, p);
-  e = cudaGetLastError();
+  e = launch_after(kern, grid, kThreads, smem, st, tq, tq32, tk, tv, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (rows * (D / 4) + 127) / 128, 1);
-  cfg.blockDim = dim3(128, 1, 1);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel<D>, p);
+  return launch_after(combine_kernel<D>, dim3(grid, (rows * (D / 4) + 127) / 128), 128, 0, st, p);
 }
 
 }  // namespace

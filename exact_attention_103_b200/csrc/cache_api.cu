@@ -30,8 +30,8 @@ attn_status_t launched(cudaError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+using attn::kMaxSequences;
 constexpr int kMaxRequests = 8192;  // slots, and requests of one alloc or fork (shared-memory lists)
-constexpr int kMaxSequences = 1024;
 constexpr int kMaxMask = 256;
 
 attn_status_t check_cache(const attn_cache_t* c) {

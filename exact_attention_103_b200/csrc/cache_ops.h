@@ -23,6 +23,30 @@ __device__ __forceinline__ void record_invalid(int* err, int site) {
   if (err) atomicCAS(err, 0, 1 | (site << 8));
 }
 
+// The serving operators follow one another on a stream in kernels of a few microseconds. Each is
+// launched as a programmatic dependent of the kernel before it and lets the next one launch at its
+// own entry; before it touches memory it waits until the kernel before it, whatever that
+// was, has completed (and with it everything earlier on the stream).
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+constexpr int kMaxSequences = 1024;  // of a packed batch
+
 struct RopeArgs {
   attn_rope_plan_t plan;  // plan.turns null: nothing is rotated
   attn_rows_t t[3];       // q, k (attn_rope: count of them; append: q, k, v)

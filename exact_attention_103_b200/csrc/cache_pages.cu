@@ -6,6 +6,7 @@
 // the order of the requests, so results never depend on timing.  All of it is
 // integer bookkeeping of a few kilobytes, bound by latency; the copies are bound by HBM.
 #include <climits>
+#include <cstring>
 #include <cuda_runtime.h>
 
 #include "cache_ops.h"
@@ -48,56 +49,85 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
 }
 
 // One fork, decided by the first kernel and carried out by the second.
-struct ForkItem {
+struct alignas(16) ForkItem {
   int src, dst, len;  // len 0: nothing to do
   int fresh;          // page of the copied tail (len % page_size != 0)
 };
 
 // Grants requests for pages.  alloc: slot a[i] grows to b[i] tokens.  FORK: slot a[i]
 // is forked into slot b[i] (the pages of its full part and the copies follow in
-// fork_kernel).  Shared memory: owner[slots] (first request that names a slot),
-// upto[n] (pages needed by requests 0..i).
+// fork_kernel).  Shared memory: owner (first request that names a slot), upto (pages
+// needed by requests 0..i), have, slot.  One block, bound by its round trips to memory: the requests
+// and the first 16384 reference counts, the lengths, the stores.
 template <bool FORK>
-__global__ void __launch_bounds__(kBlock) grant_kernel(const attn_cache_t c, const int32_t* a, const int32_t* b, int n,
-                                                       int32_t* granted, ForkItem* items, int* err) {
+__global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, const int32_t* a, const int32_t* b, int n,
+                                                          int32_t* granted, ForkItem* items, int* err) {
   extern __shared__ int shared[];
   __shared__ int warp_sums[32];
-  int* owner = shared;
-  int* upto = shared + c.slots;
+  int* owner = shared;          // [slots]
+  int* upto = owner + c.slots;  // [n]
+  int* have = upto + n;         // [n] pages held before (-1: refused)
+  int* slot = have + n;         // [n] the slot that is written
   const int tid = threadIdx.x;
   const int32_t* target = FORK ? b : a;  // the slot that is written
+  let_next_launch();
   for (int s = tid; s < c.slots; s += kBlock) owner[s] = INT_MAX;
-  __syncthreads();
-  for (int i = tid; i < n; i += kBlock) {
-    const int s = __ldg(target + i);
-    if (s >= 0 && s < c.slots) atomicMin(&owner[s], i);
-  }
-  __syncthreads();
+  wait_for_previous();
+  // The first stretch of reference counts is on its way while the requests are read.
+  const bool wide = (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0;
+  auto free_pages = [&](int p0) -> unsigned {  // bit k: page p0 + k is free
+    unsigned bits = 0;
+    if (wide && p0 + kPagesPerThread <= c.pages) {
+      int4 w[kPagesPerThread / 4];
+#pragma unroll
+      for (int k = 0; k < kPagesPerThread / 4; ++k) w[k] = __ldcg(reinterpret_cast<const int4*>(c.refs + p0) + k);
+#pragma unroll
+      for (int k = 0; k < kPagesPerThread / 4; ++k)
+        bits |= ((w[k].x == 0) | ((w[k].y == 0) << 1) | ((w[k].z == 0) << 2) | ((w[k].w == 0) << 3)) << (4 * k);
+    } else {
+      for (int k = 0; k < kPagesPerThread; ++k)
+        if (p0 + k < c.pages && __ldcg(c.refs + p0 + k) == 0) bits |= 1u << k;
+    }
+    return bits;
+  };
+  unsigned bits = free_pages(tid * kPagesPerThread);
   // Each thread takes consecutive requests, so that the prefix sum follows their order.
   const int per = (n + kBlock - 1) / kBlock;
   const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  __syncthreads();
+  for (int i = i0; i < i1; ++i) {
+    const int s = slot[i] = __ldg(target + i);
+    if (s >= 0 && s < c.slots) atomicMin(&owner[s], i);
+  }
+  __syncthreads();
   int sum = 0;
   for (int i = i0; i < i1; ++i) {
-    const int s = __ldg(target + i);
+    const int s = slot[i];
     bool ok = s >= 0 && s < c.slots && owner[s] == i;
-    int site = kSiteSlot, need = 0;
+    int site = kSiteSlot, need = 0, held = 0;
     if (FORK) {
       const int from = __ldg(a + i);
       ok = ok && from >= 0 && from < c.slots && from != s;
       if (ok) {
-        const int len = c.lens[from];
+        const int len = __ldcg(c.lens + from), there = __ldcg(c.lens + s);
         site = kSiteLength;
-        ok = c.lens[s] == 0 && len >= 0 && len <= static_cast<int64_t>(c.max_pages) * c.page_size;
-        if (ok) need = (len & (c.page_size - 1)) ? 1 : 0;
+        ok = there == 0 && len >= 0 && len <= static_cast<int64_t>(c.max_pages) * c.page_size;
+        if (ok) {
+          need = (len & (c.page_size - 1)) ? 1 : 0;
+          items[i].len = len;
+        }
       }
     } else if (ok) {
-      const int len = c.lens[s], want = __ldg(b + i);
+      const int len = __ldcg(c.lens + s), want = __ldg(b + i);
       site = kSiteLength;
       ok = len >= 0 && want >= len && want <= static_cast<int64_t>(c.max_pages) * c.page_size;
-      if (ok) need = pages_of(want, c.page_size) - pages_of(len, c.page_size);
+      if (ok) {
+        held = pages_of(len, c.page_size);
+        need = pages_of(want, c.page_size) - held;
+      }
     }
     if (!ok) record_invalid(err, site);
-    granted[i] = ok;
+    have[i] = ok ? held : -1;
     sum += need;
     upto[i] = sum;  // within the thread; the threads before are added below
   }
@@ -110,48 +140,43 @@ __global__ void __launch_bounds__(kBlock) grant_kernel(const attn_cache_t c, con
   int found = 0;
   for (int base = 0; base < c.pages && found < total; base += kBlock * kPagesPerThread) {
     const int p0 = base + tid * kPagesPerThread;
-    unsigned free_bits = 0;
-    if (p0 + kPagesPerThread <= c.pages && (reinterpret_cast<uintptr_t>(c.refs) & 15) == 0) {
-#pragma unroll
-      for (int k = 0; k < kPagesPerThread / 4; ++k) {
-        const int4 w = reinterpret_cast<const int4*>(c.refs + p0)[k];
-        free_bits |= ((w.x == 0) | ((w.y == 0) << 1) | ((w.z == 0) << 2) | ((w.w == 0) << 3)) << (4 * k);
-      }
-    } else {
-      for (int k = 0; k < kPagesPerThread; ++k)
-        if (p0 + k < c.pages && c.refs[p0 + k] == 0) free_bits |= 1u << k;
-    }
     int here;
-    int rank = found + block_scan(__popc(free_bits), warp_sums, here);
-    for (; free_bits && rank < total; ++rank, free_bits &= free_bits - 1) {
-      const int page = p0 + __ffs(free_bits) - 1;
-      int lo = 0, hi = n - 1;  // the first request with upto > rank
+    int rank = found + block_scan(__popc(bits), warp_sums, here);
+    unsigned next = 0;  // the next stretch loads behind this one's work
+    if (found + here < total && p0 + kBlock * kPagesPerThread < c.pages) next = free_pages(p0 + kBlock * kPagesPerThread);
+    int lo = 0;  // the first request with upto > rank: searched once, then followed
+    if (bits && rank < total) {
+      int hi = n - 1;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (upto[mid] > rank) hi = mid; else lo = mid + 1;
       }
+    }
+    for (; bits && rank < total; ++rank, bits &= bits - 1) {
+      const int page = p0 + __ffs(bits) - 1;
+      while (upto[lo] <= rank) ++lo;
       c.refs[page] = 1;
       if (FORK) {
         items[lo].fresh = page;
       } else {
-        const int s = __ldg(a + lo);
-        const int k = pages_of(c.lens[s], c.page_size) + rank - (lo ? upto[lo - 1] : 0);
-        c.page_table[static_cast<int64_t>(s) * c.max_pages + k] = page;
+        const int k = have[lo] + rank - (lo ? upto[lo - 1] : 0);
+        c.page_table[static_cast<int64_t>(slot[lo]) * c.max_pages + k] = page;
       }
     }
     found += here;
+    bits = next;
   }
   __syncthreads();
   for (int i = i0; i < i1; ++i) {
     const int first = i ? upto[i - 1] : 0, need = upto[i] - first;
-    bool ok = granted[i] != 0;
-    const int s = __ldg(target + i);
+    bool ok = have[i] >= 0;
+    const int s = slot[i];
     if (ok && need > 0 && upto[i] > found) {
       ok = false;
       // What it did get goes back (a fork needs one page: it got none).
       for (int k = 0; !FORK && k < found - first; ++k) {
-        int32_t* e = c.page_table + static_cast<int64_t>(s) * c.max_pages + pages_of(c.lens[s], c.page_size) + k;
-        c.refs[*e] = 0;
+        int32_t* e = c.page_table + static_cast<int64_t>(s) * c.max_pages + have[i] + k;
+        c.refs[__ldcg(e)] = 0;
         *e = -1;
       }
     }
@@ -159,14 +184,11 @@ __global__ void __launch_bounds__(kBlock) grant_kernel(const attn_cache_t c, con
     if (FORK) {
       items[i].src = __ldg(a + i);
       items[i].dst = s;
-      items[i].len = ok ? c.lens[items[i].src] : 0;
+      if (!ok) items[i].len = 0;
+      else c.lens[s] = items[i].len;
+    } else if (ok) {
+      c.lens[s] = __ldg(b + i);
     }
-  }
-  __syncthreads();  // every length has been read
-  for (int i = i0; i < i1; ++i) {
-    if (!granted[i]) continue;
-    const int s = __ldg(target + i);
-    c.lens[s] = FORK ? items[i].len : __ldg(b + i);
   }
 }
 
@@ -179,11 +201,11 @@ __device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int
   for (; i + 3 * blockDim.x < n; i += 4 * blockDim.x) {
     uint4 w[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = s[i + k * blockDim.x];
+    for (int k = 0; k < 4; ++k) w[k] = __ldcg(s + i + k * blockDim.x);
 #pragma unroll
     for (int k = 0; k < 4; ++k) d[i + k * blockDim.x] = w[k];
   }
-  for (; i < n; i += blockDim.x) d[i] = s[i];
+  for (; i < n; i += blockDim.x) d[i] = __ldcg(s + i);
 }
 
 __device__ __forceinline__ int64_t row_bytes(const attn_cache_t& c) {
@@ -198,14 +220,18 @@ __device__ __forceinline__ uint8_t* cache_row(const attn_cache_t& c, int l, int 
 // Block (i, 0) writes the table row and references of fork i; block (i, 1 + y) copies
 // the tail's tokens of one layer's K or V.
 __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* err) {
-  const ForkItem it = items[blockIdx.x];
+  let_next_launch();
+  wait_for_previous();
+  const int4 w = __ldcg(reinterpret_cast<const int4*>(items + blockIdx.x));
+  ForkItem it;
+  memcpy(&it, &w, sizeof(it));
   if (it.len <= 0) return;
   const int full = it.len / c.page_size, part = it.len & (c.page_size - 1);
   const int32_t* from = c.page_table + static_cast<int64_t>(it.src) * c.max_pages;
   if (blockIdx.y == 0) {
     int32_t* to = c.page_table + static_cast<int64_t>(it.dst) * c.max_pages;
     for (int m = threadIdx.x; m < full; m += blockDim.x) {
-      const int p = from[m];
+      const int p = __ldcg(from + m);
       if (p < 0 || p >= c.pages) record_invalid(err, kSitePage);
       else atomicAdd(c.refs + p, 1);
       to[m] = p;
@@ -214,7 +240,7 @@ __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* er
     return;
   }
   if (!part) return;
-  const int old = from[full];
+  const int old = __ldcg(from + full);
   if (old < 0 || old >= c.pages) {
     if (threadIdx.x == 0) record_invalid(err, kSitePage);
     return;
@@ -224,35 +250,52 @@ __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* er
              cache_row(c, y >> 1, y & 1, static_cast<int64_t>(it.fresh) * c.page_size), part * row_bytes(c));
 }
 
+__device__ __forceinline__ void drop(const attn_cache_t& c, int page, int* err) {
+  if (page < 0 || page >= c.pages) {
+    record_invalid(err, kSitePage);
+  } else if (atomicSub(c.refs + page, 1) <= 0) {
+    atomicAdd(c.refs + page, 1);
+    record_invalid(err, kSitePage);
+  }
+}
+
 // Takes a reference from entries [m0, m1) of a slot's table row and clears them.
 __device__ __forceinline__ void release(const attn_cache_t& c, int slot, int m0, int m1, int* err) {
   int32_t* row = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
   for (int m = m0 + threadIdx.x; m < m1; m += blockDim.x) {
-    const int p = row[m];
+    const int p = __ldcg(row + m);
     row[m] = -1;
-    if (p < 0 || p >= c.pages) {
-      record_invalid(err, kSitePage);
-    } else if (atomicSub(c.refs + p, 1) <= 0) {
-      atomicAdd(c.refs + p, 1);
-      record_invalid(err, kSitePage);
-    }
+    drop(c, p, err);
   }
 }
 
 __global__ void free_kernel(const attn_cache_t c, const int32_t* slots, int* err) {
   __shared__ int len;
+  let_next_launch();
+  wait_for_previous();
   const int slot = __ldg(slots + blockIdx.x);
   if (slot < 0 || slot >= c.slots) {
     if (threadIdx.x == 0) record_invalid(err, kSiteSlot);
     return;
   }
+  // The first entries of the row load beside the length.
+  int32_t* row = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
+  const int m = threadIdx.x;
+  const int p = m < c.max_pages ? __ldcg(row + m) : 0;
   if (threadIdx.x == 0) len = atomicExch(c.lens + slot, 0);  // named twice: the second finds 0
   __syncthreads();
   if (len <= 0) return;
-  release(c, slot, 0, min(pages_of(len, c.page_size), c.max_pages), err);
+  const int count = min(pages_of(len, c.page_size), c.max_pages);
+  if (m < count) {
+    row[m] = -1;
+    drop(c, p, err);
+  }
+  release(c, slot, blockDim.x, count, err);
 }
 
 __global__ void copy_kernel(const attn_cache_t c, const int32_t* src, const int32_t* dst, int n, int chunks, int* err) {
+  let_next_launch();
+  wait_for_previous();
   const int i = blockIdx.x;
   const int from = __ldg(src + i), to = __ldg(dst + i);
   if (from < 0 || from >= c.pages || to < 0 || to >= c.pages) {
@@ -285,7 +328,7 @@ struct Kept {
   bool ok;
 };
 __device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
-                                        const int32_t* accepted, const int32_t* slots, int b, int* err) {
+                                        const int32_t* accepted, const int32_t* slots, int b, int* err) {  // err null: another kernel says it
   Kept k;
   k.slot = slots ? __ldg(slots + b) : b;
   int bad = 0;
@@ -294,7 +337,7 @@ __device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu
     k.len = k.base = k.count = 0;
   } else {
     const int n = __ldg(cu_q + b + 1) - __ldg(cu_q + b);
-    k.len = c.lens[k.slot];
+    k.len = __ldcg(c.lens + k.slot);
     k.count = __ldg(accepted + b);
     k.base = k.len - n;
     if (n < 0 || k.base < 0 || k.len > static_cast<int64_t>(c.max_pages) * c.page_size) bad = kSiteLength;
@@ -309,7 +352,7 @@ __device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu
     for (int j = threadIdx.x; slots && j < b; j += blockDim.x)
       if (__ldg(slots + j) == k.slot) bad = kSiteSlot;
   }
-  if (bad) record_invalid(err, bad);
+  if (bad && err) record_invalid(err, bad);
   k.ok = !__syncthreads_or(bad);
   return k;
 }
@@ -323,8 +366,10 @@ constexpr int kMoves = 128;  // moves whose rows are looked up together
 __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
                                const int32_t* accepted, const int32_t* slots, int* err) {
   __shared__ int64_t from[kMoves], to[kMoves];
+  let_next_launch();
+  wait_for_previous();
   const int b = blockIdx.x;
-  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, b, err);
+  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, b, nullptr);  // cut_kernel reports
   if (!k.ok) return;
   const int l = blockIdx.y >> 1, kv = blockIdx.y & 1;
   const int64_t rb = row_bytes(c);
@@ -336,7 +381,7 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
     __syncthreads();
     for (int i = threadIdx.x; i < m; i += blockDim.x) {
       const int x = k.base + __ldg(path + static_cast<int64_t>(b) * width + m0 + i), y = k.base + m0 + i;
-      const int px = row[x / c.page_size], py = row[y / c.page_size];
+      const int px = __ldcg(row + x / c.page_size), py = __ldcg(row + y / c.page_size);
       const bool ok = px >= 0 && px < c.pages && py >= 0 && py < c.pages;
       if (!ok) record_invalid(err, kSitePage);
       from[i] = (ok && x != y) ? static_cast<int64_t>(px) * c.page_size + (x & (c.page_size - 1)) : -1;
@@ -348,7 +393,7 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
       uint4 w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (i + j < m && from[i + j] >= 0) w[j] = *reinterpret_cast<const uint4*>(base + from[i + j] * rb);
+        if (i + j < m && from[i + j] >= 0) w[j] = __ldcg(reinterpret_cast<const uint4*>(base + from[i + j] * rb));
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (i + j < m && from[i + j] >= 0) *reinterpret_cast<uint4*>(base + to[i + j] * rb) = w[j];
@@ -358,6 +403,8 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
 
 __global__ void cut_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
                            const int32_t* accepted, const int32_t* slots, int* err) {
+  let_next_launch();
+  wait_for_previous();  // the moves have read the table
   const Kept k = kept_of(c, cu_q, path, width, accepted, slots, blockIdx.x, err);
   if (!k.ok) return;
   __syncthreads();  // every thread has read the length
@@ -374,29 +421,25 @@ static cudaError_t grant_smem(const void* kern, size_t smem) {
 
 cudaError_t launch_alloc(const attn_cache_t& c, const int32_t* slots, const int32_t* want, int n, int32_t* granted,
                          int* err, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(c.slots) + n) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(c.slots) + 3 * n) * sizeof(int);
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<false>), smem);
   if (e != cudaSuccess) return e;
-  grant_kernel<false><<<1, kBlock, smem, st>>>(c, slots, want, n, granted, nullptr, err);
-  return cudaGetLastError();
+  return launch_after(grant_kernel<false>, 1, kBlock, smem, st, c, slots, want, n, granted, static_cast<ForkItem*>(nullptr), err);
 }
 
 cudaError_t launch_free(const attn_cache_t& c, const int32_t* slots, int n, int* err, cudaStream_t st) {
-  free_kernel<<<n, 128, 0, st>>>(c, slots, err);
-  return cudaGetLastError();
+  return launch_after(free_kernel, n, 128, 0, st, c, slots, err);
 }
 
 cudaError_t launch_fork(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int32_t* granted,
                         void* ws, int* err, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(c.slots) + n) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(c.slots) + 3 * n) * sizeof(int);
   cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<true>), smem);
   if (e != cudaSuccess) return e;
   ForkItem* items = static_cast<ForkItem*>(ws);
-  grant_kernel<true><<<1, kBlock, smem, st>>>(c, src, dst, n, granted, items, err);
-  e = cudaGetLastError();
+  e = launch_after(grant_kernel<true>, 1, kBlock, smem, st, c, src, dst, n, granted, items, err);
   if (e != cudaSuccess) return e;
-  fork_kernel<<<dim3(n, 1 + 2 * c.layers), 256, 0, st>>>(c, items, err);
-  return cudaGetLastError();
+  return launch_after(fork_kernel, dim3(n, 1 + 2 * c.layers), 256, 0, st, c, items, err);
 }
 
 cudaError_t launch_copy(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int* err, cudaStream_t st) {
@@ -409,8 +452,7 @@ cudaError_t launch_copy(const attn_cache_t& c, const int32_t* src, const int32_t
   int parts = 4096 / n;
   if (parts > c.layers * 2 * chunks) parts = c.layers * 2 * chunks;
   if (parts < 1) parts = 1;
-  copy_kernel<<<dim3(n, parts), 256, 0, st>>>(c, src, dst, n, chunks, err);
-  return cudaGetLastError();
+  return launch_after(copy_kernel, dim3(n, parts), 256, 0, st, c, src, dst, n, chunks, err);
 }
 
 cudaError_t launch_compact(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
@@ -418,11 +460,9 @@ cudaError_t launch_compact(const attn_cache_t& c, const int32_t* cu_q, const int
   const int64_t words = static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2) / 16;
   const int threads = words >= 256 ? 256 : static_cast<int>((words + 31) / 32 * 32);
   const int z = static_cast<int>((words + threads - 1) / threads);
-  compact_kernel<<<dim3(B, 2 * c.layers, z), threads, 0, st>>>(c, cu_q, path, width, accepted, slots, err);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(compact_kernel, dim3(B, 2 * c.layers, z), threads, 0, st, c, cu_q, path, width, accepted, slots, err);
   if (e != cudaSuccess) return e;
-  cut_kernel<<<B, 128, 0, st>>>(c, cu_q, path, width, accepted, slots, err);
-  return cudaGetLastError();
+  return launch_after(cut_kernel, B, 128, 0, st, c, cu_q, path, width, accepted, slots, err);
 }
 
 }  // namespace attn
