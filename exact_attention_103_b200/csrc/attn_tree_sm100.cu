@@ -12,26 +12,34 @@
 //  - The query heads that share a cache head, and all drafted tokens, are packed into the rows
 //    of one item: row r of a 128-row tile is token r / G, head r % G of the group (G = Hq /
 //    heads), so K and V are read once for all of them.
-//  - Work is dealt in equal numbers of 128-key tiles: the tiles of all (sequence, cache head, row
-//    pair) items form one list, and CTA c of the grid takes the c-th equal part.  One long
+//  - Work is dealt in equal costs: the 128-key tiles of all (sequence, cache head, row pair)
+//    items form one list, and CTA c of the grid takes the c-th equal part.  One long
 //    sequence fills every SM as well as many short ones do.  A part that begins or ends
 //    inside an item leaves its rows' unnormalised O (fp32), maximum and sum in the workspace; a
 //    CTA leaves at most two of those.  combine_kernel joins them in a fixed order.
-//  - An item of up to 128 rows runs its key tiles alternately through the two softmax
-//    warpgroups (tile j in stream j % 2, each with its own S and O in TMEM, joined at the
-//    end), so that one tile's softmax overlaps the other's products.  An item of 129 to 256 rows
-//    gives each warpgroup its own 128 rows of every key tile.
+//  - An item of up to 128 rows gives each of the two softmax warpgroups (streams, with an O of
+//    their own in TMEM, joined at the end) one half of every key tile, so that one's softmax
+//    overlaps the other's products.  An item of 129 to 256 rows gives each its own 128 rows of every
+//    key tile.
+//  - Few rows leave most threads of a row-per-thread softmax idle: up to 32 rows the scores are
+//    computed transposed, a key per thread (swapped items).
 //
 // E4M3 caches: the keys and values go to the tensor cores as they are (kind::f8f6f4), and the
 // other operand of each product is split into two E4M3 terms, hi + lo, which keeps bf16's
 // precision: a bf16 query scaled by a power of two (its row's largest value in [128, 256)) is
-// hi + lo exactly down to 2^-9 of that scale, and hi + lo holds P~ to 2^-8 (the first term keeps 4
-// significant bits, the second 4 more).  Each costs one more product, at twice bf16's rate.
+// hi + lo to 2^-9 of that scale, and hi + lo holds P~ to 2^-8 (the first term keeps 4
+// significant bits, the second 4 more).  Each costs one more product, at twice bf16's rate; up to
+// 64 rows both terms are rows of one product (duo items), or columns of it (swapped items).
 //
 // Warp roles (384 threads): 0-3 and 4-7 softmax, correction and epilogue of streams 0 and 1;
 // 8 and 10 TMA producers of K (and q) and of V; 9 (TMEM owner) and 11 issue S and P~V.  The softmax
 // warps write an E4M3 cache's split queries.  Every wait is bounded; on expiry the CTA stops, drains its
 // copies and products, frees TMEM and returns.
+//
+// Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
+// 64 ragged contexts of 512 to 8192, one token, bf16: 146 (86%).  Two contexts of 131072, 64 rows,
+// E4M3: 140 (56%; the softmax with its conversions bounds it).  A call of little work costs
+// 11 to 13: two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -62,6 +70,9 @@ __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8
 // heads a cache head, bf16 / E4M3, us): 32 rows 65 / 58 transposed; 64 rows 80 / 81 transposed, 73 / 68
 // as one row tile, where every row has a thread and its reference stays in a register.
 constexpr int kSwapped = 32;
+// E4M3 items above that and up to 64 rows: see Seg::duo.  Measured (two contexts of 131072, 64 rows,
+// us): 158 with both terms as products of their own, 140.
+constexpr int kDuo = 64;
 constexpr int kMinPart = 4;  // no CTA takes less of the list: the longest tile
 
 struct TreeParams {
@@ -123,7 +134,7 @@ struct Layout {
   static constexpr int TABLE_OFF = MISC_OFF + 128;
   // Cost of a key tile with one and with two row tiles (the copies bound the first, the softmax of
   // 256 rows the second), and of beginning an item.
-  static constexpr int COST_ONE = ESZ * D == 256 ? 3 : 2, COST_PAIR = ESZ * D == 256 ? 4 : 4, COST_ITEM = ESZ * D == 256 ? 10 : 12;
+  static constexpr int COST_ONE = 2, COST_PAIR = ESZ * D == 256 ? 3 : 4, COST_ITEM = ESZ * D == 256 ? 7 : 12;
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -144,6 +155,9 @@ struct Seg {
   int begin, next;        // where the item begins in the list, and the next stretch
   bool two;               // more than one row tile
   bool swapped;           // at most kSwapped rows
+  // E4M3, at most kDuo rows: the two terms of a split operand are rows of one product, hi of row i
+  // in lane 32 (i / 16) + i % 16, lo 16 lanes behind; two threads of the warp share the row.
+  bool duo;
 };
 
 // The list of work, decoded alike by every role: items (sequence, cache head, row pair) one
@@ -154,7 +168,7 @@ struct Seg {
 struct List {
   const int *cum, *cu, *slot, *len;
   int B, heads, G, tpt, one, pair, item;
-  bool masked;
+  bool masked, split;
 
   // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
   // than itself.
@@ -190,6 +204,7 @@ struct List {
     s.nt = min(2 * tpt, s.n - s.tok0);
     s.two = s.nt > tpt;
     s.swapped = s.nt * G <= kSwapped;
+    s.duo = split && !s.swapped && s.nt * G <= kDuo;
     s.kvt = kv;
     s.begin = x - r;
     s.next = min(end, s.begin + item + kv * w);
@@ -199,27 +214,24 @@ struct List {
   }
 };
 
-// The products run as units of 64 keys, S(u) four units ahead of P~V(u); unit u belongs to stream
-// u % 2, and its S (then P~) lies in buffer u % 4, so that a stream finds its next S computed
-// while it works on one.  Two row tiles: the streams take the same half tiles; one: stream s
-// takes tiles j0 + s, j0 + s + 2, ...  A second half that lies behind the sequence's end is
-// left out.
+// The products run as units of 64 keys, in rounds of one unit for each stream, S(v) two rounds
+// ahead of P~V(v); round v's S (then P~) lie in buffers 2 (v % 2) and the next one, so that a
+// stream finds its next S computed while it works on one.  Two row tiles: both streams take the
+// same half tile, two rounds a tile; one: stream s takes half s, a round a tile, so that a tile's slot
+// is soon free again.  A second half that lies behind the sequence's end is left out.
 struct Unit {
   int j, half;  // tile (from j0) and half
   bool live;
 };
-__device__ __forceinline__ Unit unit_at(const Seg& it, int u) {
-  const int v = u >> 1, s = u & 1, nj = it.j1 - it.j0;
+__device__ __forceinline__ bool full_tile(const Seg& it, int j) { return it.len - (it.j0 + j) * kBN > kBN / 2; }
+__device__ __forceinline__ Unit unit_at(const Seg& it, int v, int s) {
   Unit x;
-  x.half = v & 1;
-  x.j = it.two ? v >> 1 : 2 * (v >> 1) + s;
-  x.live = x.j < nj && (x.half == 0 || it.len - (it.j0 + x.j) * kBN > kBN / 2);
+  x.half = it.two ? v & 1 : s;
+  x.j = it.two ? v >> 1 : v;
+  x.live = x.half == 0 || full_tile(it, x.j);
   return x;
 }
-__device__ __forceinline__ int unit_count(const Seg& it) {
-  const int nj = it.j1 - it.j0;
-  return 4 * (it.two ? nj : (nj + 1) / 2);
-}
+__device__ __forceinline__ int rounds_of(const Seg& it) { return (it.two ? 2 : 1) * (it.j1 - it.j0); }
 
 __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   const uint64_t t0 = global_timer_ns();
@@ -228,6 +240,8 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
   }
   return true;
 }
+
+constexpr uint32_t kLoLanes = 16u << 16;  // from the hi rows of a duo item to its lo rows, as a TMEM address
 
 // Rows of a swapped item's products.
 __device__ __forceinline__ int swapped_rows(int rows) { return rows <= 16 ? 16 : 32; }
@@ -332,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   list.pair = Lay::COST_PAIR;
   list.item = Lay::COST_ITEM;
   list.masked = p.mask != nullptr;
+  list.split = F8;
   {
     // The tiles of each sequence and their prefix sum; a thread takes consecutive sequences.
     const int per = ceil_div(p.B, kThreads);
@@ -436,62 +451,66 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = (it.two ? (k ? it.nt - p.tpt : p.tpt) : it.nt) * p.G;
       const int64_t tok = it.q0 + it.tok0 + k * p.tpt;
       uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
-      // A row is held by D / 8 lanes, 8 values each; 4 steps are in flight together.
+      // A row is held by D / 8 lanes, 8 values each.  Four rows' loads are in flight; the loop is not
+      // unrolled, as its code runs cold at the head of an item, where fetching it is what counts.
       constexpr int L = D / 8, R = 32 / L, U = 4;
       const int c = lane % L;
-      for (int r0 = w8 * R + lane / L; __any_sync(0xffffffffu, r0 < rows); r0 += 8 * R * U) {
-        uint4 w[U];
+      auto fetch = [&](int r) {
+        const int t = r / p.G;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < rows) w = __ldcg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + (r - t * p.G)) * D) + c);
+        return w;
+      };
+      int r = w8 * R + lane / L;
+      uint4 w[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int r = r0 + 8 * R * i, t = r / p.G, gg = r - t * p.G;
-          w[i] = make_uint4(0, 0, 0, 0);
-          if (r < rows) w[i] = __ldcg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + gg) * D) + c);
+      for (int i = 0; i < U; ++i) w[i] = fetch(r + 8 * R * i);
+#pragma unroll 1
+      for (; __any_sync(0xffffffffu, r < rows); r += 8 * R) {
+        const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+        for (int i = 0; i + 1 < U; ++i) w[i] = w[i + 1];
+        w[U - 1] = fetch(r + 8 * R * U);
+        float v[8];
+        float top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __uint_as_float(u[e] << 16);
+          v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+          top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
         }
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int r = r0 + 8 * R * i;
-          if (!__any_sync(0xffffffffu, r < rows)) break;
-          float v[8];
-          const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-          float top = 0.f;
+        for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+        e = max(-100, min(e, 120));
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+        uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(u[e] << 16);
-            v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+        for (int y = 0; y < 2; ++y) {
+          hi[y] = lo[y] = 0;
+#pragma unroll
+          for (int z = 0; z < 2; ++z) {
+            const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
+            float ha, hb;
+            upper4_x2(ha, hb, a, b);
+            hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
+            lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
           }
-#pragma unroll
-          for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
-          int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          e = max(-100, min(e, 120));
-          const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-          uint32_t hi[2], lo[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            hi[y] = lo[y] = 0;
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
-              float ha, hb;
-              upper4_x2(ha, hb, a, b);
-              hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
-              lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
-            }
-          }
-          if (r < rows) {
-            if (c == 0)
-              qs[slot * kBM + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-            // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
-            // lo rows follow its hi rows: both are columns of one product.
-            auto at = [&](int row) {
-              return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
-                                      : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
-            };
-            uint8_t* lo_at = it.swapped ? base + at(r + swapped_rows(rows)) : base + Lay::TILE + at(r);
-            *reinterpret_cast<uint2*>(base + at(r)) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
-          }
+        }
+        if (r < rows) {
+          if (c == 0)
+            qs[slot * kBM + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+          // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
+          // lo rows follow its hi rows: both are columns of one product.
+          auto at = [&](int row) {
+            return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
+                                    : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
+          };
+          const int row = it.duo ? 32 * (r >> 4) + (r & 15) : r;
+          uint8_t* lo_at = it.swapped ? base + at(r + swapped_rows(rows)) : it.duo ? base + at(row + 16) : base + Lay::TILE + at(r);
+          *reinterpret_cast<uint2*>(base + at(row)) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
         }
       }
       fence_proxy_async_smem();
@@ -598,7 +617,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = wq * 32 + lane;
     const uint32_t lane_bits = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t t_o = tmem + lane_bits + (s ? Lay::TM_O1 : Lay::TM_O0);
-    const int tl = r / p.G, g = r - tl * p.G;  // token of the tile, head of the group
     float2* ml = reinterpret_cast<float2*>(smem + Lay::ML_OFF);
     uint32_t phases = 0;  // bit u & 3: phase of that buffer's next use
     uint32_t o_phase = 0, m_phase = 0, e_phase = 0;
@@ -886,24 +904,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     bool ok = true;
-    int4 hd = make_int4(-1, 0, 0, 0);  // the item whose first tiles this CTA holds without its last
+    if (threadIdx.x == 0) p.head[cta] = make_int4(-1, 0, 0, 0);
     for (int x = x0; x < x1 && ok;) {
       const Seg it = list.at(x, x1);
       x = it.next;
       if (it.j0 >= it.j1) continue;
-      if (it.j0 == 0 && it.j1 < it.kvt) {
-        // the CTA whose part holds the first unit of the item's last tile
+      if (threadIdx.x == 0 && it.j0 == 0 && it.j1 < it.kvt) {
+        // The item's first tiles without its last: the CTA whose part holds the first unit of the item's last tile
         const int64_t end = it.begin + list.item + (it.kvt - 1) * (it.two ? list.pair : list.one);
         int last = static_cast<int>(end * ctas / total);
         while (static_cast<int64_t>(last + 1) * total / ctas <= end) ++last;
         while (static_cast<int64_t>(last) * total / ctas > end) --last;
-        hd = make_int4(it.q0 + it.tok0, it.h, it.nt, last);
+        p.head[cta] = make_int4(it.q0 + it.tok0, it.h, it.nt, last);
       }
       const int first = it.two ? s * p.tpt : 0;  // this stream's first token of the item
       const int mine = it.two ? (s ? it.nt - p.tpt : p.tpt) : it.nt;
-      const int tok = it.tok0 + first + tl;      // this row's token of the sequence
+      // The warp's rows of the tile, this thread's row of it, and that row's token.
+      const int row_n = it.duo ? 16 : 32, row0 = wq * row_n, rr = row0 + (lane & (row_n - 1));
+      const int tl = rr / p.G;
+      const int tok = it.tok0 + first + tl;  // of the sequence
       const bool valid = tl < mine;
-      const bool busy = wq * 32 < mine * p.G;    // the warp has a valid row
+      const bool busy = row0 < mine * p.G;   // the warp has a valid row
       float sl = p.scale_log2;
       if constexpr (F8) {
         ok = split_q(it, nq, warp);
@@ -912,11 +933,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int mine_q = nq + (it.two ? s : 0);
         ok = wait(Lay::B_QFULL + (mine_q & 1), (mine_q >> 1) & 1, kSiteTQFull);
         if (!ok) break;
-        sl = reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + r];
+        sl = reinterpret_cast<const float*>(smem + Lay::QS_OFF)[(mine_q & 1) * kBM + rr];
       }
       if (p.mask != nullptr && it.j1 * kBN > it.ctx) {
         // The mask rows of this warp's tokens will be needed for the last tiles.
-        const int t0 = it.swapped ? 0 : (wq * 32) / p.G, t1 = it.swapped ? it.nt - 1 : min((wq * 32 + 31) / p.G, mine - 1);
+        const int t0 = it.swapped ? 0 : row0 / p.G, t1 = it.swapped ? it.nt - 1 : min((row0 + row_n - 1) / p.G, mine - 1);
         const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first + t0) * p.mask_width;
         for (int i = lane * 128; i < (t1 - t0 + 1) * p.mask_width; i += 32 * 128)
           asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + i));
@@ -934,148 +955,173 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = -INFINITY, l = 0.f;
       bool any = false;
       int last_buf = 0;  // buffer of the stream's last unit
-      const int units = unit_count(it);
-      for (int u = s; u < units; u += 2) {
-        const Unit un = unit_at(it, u);
-        if (!un.live) continue;
-        const int buf = u & 3;
-        const uint32_t t_s = tmem + lane_bits + Lay::TM_S + 64 * buf;
-        ok = wait(Lay::B_SFULL + buf, (phases >> buf) & 1u, kSiteTSFull);
-        if (!ok) break;
-        phases ^= 1u << buf;
-        tc_fence_after();
-        auto release = [&]() {
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(Lay::B_PFULL + buf));
-        };
-        const bool again = any;  // O holds something
-        any = true;
-        if (!busy) {  // nothing to compute: the rows of P~ that stay behind are never read
-          release();
-          last_buf = buf;
-          continue;
-        }
-        uint32_t sa[64];
-        tmem_ld_x64(t_s, sa);
-        const int kb = (it.j0 + un.j) * kBN + 64 * un.half;
-        if (kb + 64 > it.ctx) {  // the half tile holds drafted tokens, or ends behind them
-          uint32_t vis[2];
-          if (p.mask == nullptr) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx + tok + 1 - kb, c);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx - kb, c);
-            // The mask rows of the warp's tokens, 32 columns per load, 8 tokens at a time.
-            const int t_lo = (wq * 32) / p.G, t_hi = min((wq * 32 + 31) / p.G, mine - 1);
-            const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first) * p.mask_width;
-            const int col = kb + lane - it.ctx;
-            for (int t0 = t_lo; t0 <= t_hi; t0 += 8) {
-              uint8_t w[8][2];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const int jl = col + 32 * c;
-                  w[i][c] = (t0 + i <= t_hi && jl >= 0 && jl < it.n)
-                                ? __ldg(rows + static_cast<int64_t>(t0 + i) * p.mask_width + jl)
-                                : 0;
-                }
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const uint32_t bits = __ballot_sync(0xffffffffu, w[i][c] != 0);
-                  if (t0 + i == tl) vis[c] |= bits;
-                }
-            }
+      const int rounds = rounds_of(it);
+      // W threads share a row, 64 / W keys of a unit each.
+      auto attend = [&](auto threads) -> bool {
+        constexpr int W = decltype(threads)::value, NC = 64 / W;
+        for (int v = 0; v < rounds; ++v) {
+          const Unit un = unit_at(it, v, s);
+          if (!un.live) continue;
+          const int buf = 2 * (v & 1) + s;
+          const uint32_t t_s = tmem + lane_bits + Lay::TM_S + 64 * buf;
+          if (!wait(Lay::B_SFULL + buf, (phases >> buf) & 1u, kSiteTSFull)) return false;
+          phases ^= 1u << buf;
+          tc_fence_after();
+          auto release = [&]() {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(Lay::B_PFULL + buf));
+          };
+          const bool again = any;  // O holds something
+          any = true;
+          if (!busy) {  // nothing to compute: the rows of P~ that stay behind are never read
+            release();
+            last_buf = buf;
+            continue;
           }
+          uint32_t sa[NC];
+          if constexpr (W == 1) {
+            tmem_ld_x64(t_s, sa);
+          } else {
+            uint32_t lo[NC];
+            tmem_ld_duo(t_s, sa);
+            tmem_ld_duo(t_s + kLoLanes, lo);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!((vis[c >> 5] >> (c & 31)) & 1u)) sa[c] = __float_as_uint(-INFINITY);
-        }
-        float m4[4];
+            for (int c = 0; c < NC; ++c) sa[c] = __float_as_uint(__uint_as_float(sa[c]) + __uint_as_float(lo[c]));
+          }
+          const int kb = (it.j0 + un.j) * kBN + 64 * un.half;
+          if (kb + 64 > it.ctx) {  // the half tile holds drafted tokens, or ends behind them
+            uint32_t vis[2];
+            if (p.mask == nullptr) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m4[i] = fmax3(__uint_as_float(sa[i]), __uint_as_float(sa[i + 4]), __uint_as_float(sa[i + 8]));
+              for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx + tok + 1 - kb, c);
+            } else {
 #pragma unroll
-        for (int c = 12; c < 60; c += 8)
+              for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx - kb, c);
+              // The mask rows of the warp's tokens, 32 columns per load, 8 tokens at a time.
+              const int t_lo = row0 / p.G, t_hi = min((row0 + row_n - 1) / p.G, mine - 1);
+              const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first) * p.mask_width;
+              const int col = kb + lane - it.ctx;
+              for (int t0 = t_lo; t0 <= t_hi; t0 += 8) {
+                uint8_t w[8][2];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const int jl = col + 32 * c;
+                    w[i][c] = (t0 + i <= t_hi && jl >= 0 && jl < it.n)
+                                  ? __ldg(rows + static_cast<int64_t>(t0 + i) * p.mask_width + jl)
+                                  : 0;
+                  }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const uint32_t bits = __ballot_sync(0xffffffffu, w[i][c] != 0);
+                    if (t0 + i == tl) vis[c] |= bits;
+                  }
+              }
+            }
+            if (W == 2 && lane >= 16) vis[0] = vis[1];
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+              if (!((vis[c >> 5] >> (c & 31)) & 1u)) sa[c] = __float_as_uint(-INFINITY);
+          }
+          float m4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            m4[i] = fmax3(m4[i], __uint_as_float(sa[c + i]), __uint_as_float(sa[c + 4 + i]));
+            m4[i] = fmax3(__uint_as_float(sa[i]), __uint_as_float(sa[i + 4]), __uint_as_float(sa[i + 8]));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(sa[60 + i]));
-        const float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]) * sl;
-        bool need = false;
-        float alpha = 1.f;
-        if (m_ref == -INFINITY) {  // the first keys that this row sees
-          m_ref = m_tile;
-        } else if (m_tile - m_ref > p.tau) {
-          need = valid;
-          alpha = fast_exp2(m_ref - m_tile);
-          m_ref = m_tile;
-          l *= alpha;
-        }
-        float nm = m_ref == -INFINITY ? 0.f : -m_ref;
-        if constexpr (F8) nm += p.p_shift;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
-        auto exps = [&](int c, float& a, float& e) {  // column pair c (keys 2c, 2c + 1)
-          ffma2_bc(a, e, __uint_as_float(sa[2 * c]), __uint_as_float(sa[2 * c + 1]), sl, nm);
-          a = fast_exp2(a);
-          e = fast_exp2(e);
-          if (c & 1) fadd2_acc(ls[2], ls[3], a, e);
-          else fadd2_acc(ls[0], ls[1], a, e);
-        };
-        if constexpr (!F8) {
-          uint32_t pk[32];
+          for (int c = 12; c < NC - 4; c += 8)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a, e;
-            exps(c, a, e);
-            pk[c] = pack_bf16x2(a, e);
+            for (int i = 0; i < 4; ++i)
+              m4[i] = fmax3(m4[i], __uint_as_float(sa[c + i]), __uint_as_float(sa[c + 4 + i]));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(m4[i], __uint_as_float(sa[NC - 4 + i]));
+          float m_tile = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+          if constexpr (W == 2) m_tile = fmaxf(m_tile, __shfl_xor_sync(0xffffffffu, m_tile, 16));
+          m_tile *= sl;
+          bool need = false;
+          float alpha = 1.f;
+          if (m_ref == -INFINITY) {  // the first keys that this row sees
+            m_ref = m_tile;
+          } else if (m_tile - m_ref > p.tau) {
+            need = valid;
+            alpha = fast_exp2(m_ref - m_tile);
+            m_ref = m_tile;
+            l *= alpha;
           }
-          tmem_st_x32(t_s, pk);
-        } else {
-          // P~ = hi + lo; the conversion of hi is exact while it is a normal E4M3 number.
-          uint32_t hi[16], lo[16];
+          float nm = m_ref == -INFINITY ? 0.f : -m_ref;
+          if constexpr (F8) nm += p.p_shift;
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          auto exps = [&](int c, float& a, float& e) {  // column pair c (keys 2c, 2c + 1)
+            ffma2_bc(a, e, __uint_as_float(sa[2 * c]), __uint_as_float(sa[2 * c + 1]), sl, nm);
+            a = fast_exp2(a);
+            e = fast_exp2(e);
+            if (c & 1) fadd2_acc(ls[2], ls[3], a, e);
+            else fadd2_acc(ls[0], ls[1], a, e);
+          };
+          if constexpr (!F8) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float a, e;
-            exps(c, a, e);
-            float ha, he, la, le;
-            upper4_x2(ha, he, a, e);
-            fsub2(la, le, a, e, ha, he);
-            const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(la, le);
-            if (c & 1) {
-              hi[c >> 1] |= wh << 16;
-              lo[c >> 1] |= wl << 16;
+            for (int c = 0; c < 32; ++c) {
+              float a, e;
+              exps(c, a, e);
+              pk[c] = pack_bf16x2(a, e);
+            }
+            tmem_st_x32(t_s, pk);
+          } else {
+            // P~ = hi + lo; the conversion of hi is exact while it is a normal E4M3 number.
+            uint32_t hi[NC / 4], lo[NC / 4];
+#pragma unroll
+            for (int c = 0; c < NC / 2; ++c) {
+              float a, e;
+              exps(c, a, e);
+              float ha, he, la, le;
+              upper4_x2(ha, he, a, e);
+              fsub2(la, le, a, e, ha, he);
+              const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(la, le);
+              if (c & 1) {
+                hi[c >> 1] |= wh << 16;
+                lo[c >> 1] |= wl << 16;
+              } else {
+                hi[c >> 1] = wh;
+                lo[c >> 1] = wl;
+              }
+            }
+            if constexpr (W == 1) {
+              tmem_st_x16(t_s, hi);
+              tmem_st_x16(t_s + 16, lo);
             } else {
-              hi[c >> 1] = wh;
-              lo[c >> 1] = wl;
+              tmem_st_duo(t_s, hi);
+              tmem_st_duo(t_s + kLoLanes, lo);
             }
           }
-          tmem_st_x16(t_s, hi);
-          tmem_st_x16(t_s + 16, lo);
-        }
-        if (again && __any_sync(0xffffffffu, need)) {
-          // the stream's last P~V has to be in O before O is rescaled
-          ok = wait(Lay::B_PVDONE + last_buf, ((phases >> last_buf) & 1u) ^ 1u, kSiteTPvDone);
-          if (!ok) break;
-          tc_fence_after();
+          if (again && __any_sync(0xffffffffu, need)) {
+            // the stream's last P~V has to be in O before O is rescaled
+            if (!wait(Lay::B_PVDONE + last_buf, ((phases >> last_buf) & 1u) ^ 1u, kSiteTPvDone)) return false;
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tmem_ld_x32(t_o + 32 * c, ov);
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t ov[32];
+              tmem_ld_x32(t_o + 32 * c, ov);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
-            tmem_st_x32(t_o + 32 * c, ov);
+              for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+              tmem_st_x32(t_o + 32 * c, ov);
+            }
           }
+          last_buf = buf;
+          release();
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         }
-        last_buf = buf;
-        release();
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if constexpr (W == 2) l += __shfl_xor_sync(0xffffffffu, l, 16);
+        return true;
+      };
+      if constexpr (F8) {
+        ok = it.duo ? attend(std::integral_constant<int, 2>{}) : attend(std::integral_constant<int, 1>{});
+      } else {
+        ok = attend(std::integral_constant<int, 1>{});
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
@@ -1102,51 +1148,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const bool whole = it.j0 == 0 && it.j1 == it.kvt;
       if (busy) {
+        const int g = rr - tl * p.G;
         const int64_t row = static_cast<int64_t>(it.q0 + tok) * p.Hq + it.h * p.G + g;
         const int64_t slot = static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0);
-        const int slot_row = (it.two ? s * kBM : 0) + r;
+        const int slot_row = (it.two ? s * kBM : 0) + rr;
         float4* part = reinterpret_cast<float4*>(p.part) + slot * (2 * kBM) * (D / 4) + slot_row;
         const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
         // Columns of this warpgroup; a stream that took no tile has nothing in its O.
         const int c_lo = it.two ? 0 : s * (D / 64), c_hi = it.two ? D / 32 : (s + 1) * (D / 64);
-        const bool use_own = any, use_other = !it.two && (s != 0 || it.j1 - it.j0 > 1);
+        const bool use_own = any, use_other = !it.two && (s != 0 || it.j1 - it.j0 > 1 || full_tile(it, 0));
         const uint32_t t_x = tmem + lane_bits + (s ? Lay::TM_O0 : Lay::TM_O1);
-        for (int c = c_lo; c < c_hi; ++c) {
-          uint32_t ov[32];
-          float v[32];
-          if (use_own) {
-            tmem_ld_x32(t_o + 32 * c, ov);
+        auto write = [&](auto threads) {
+          constexpr int W = decltype(threads)::value, NV = 32 / W;  // columns of a thread, of 32
+          const int mine_at = W == 2 ? lane & 16 : 0;
+          for (int c = c_lo; c < c_hi; ++c) {
+            uint32_t ov[NV];
+            float v[NV];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(ov[i]) * a0;
-          } else {
+            for (int i = 0; i < NV; ++i) v[i] = 0.f;
+            auto add = [&](uint32_t at, float weight) {
+              if constexpr (W == 1) tmem_ld_x32(at + 32 * c, ov);
+              else tmem_ld_duo(at + 32 * c, ov);
+              // weight 0 also where the stream's O was never a number
+              if (weight != 0.f) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0.f;
-          }
-          if (use_other) {
-            tmem_ld_x32(t_x + 32 * c, ov);
-            // weight 0 also where the other stream's O was never a number
-            if (a1 != 0.f) {
+                for (int i = 0; i < NV; ++i) v[i] = fmaf(__uint_as_float(ov[i]), weight, v[i]);
+              }
+            };
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = fmaf(__uint_as_float(ov[i]), a1, v[i]);
+            for (int term = 0; term < W; ++term) {
+              if (use_own) add(t_o + term * kLoLanes, a0);
+              if (use_other) add(t_x + term * kLoLanes, a1);
             }
-          }
-          if (valid && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + 32 * c);
+            if (valid && whole) {
+              uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + 32 * c + mine_at);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
-                                  pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
-                                  pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
-                                  pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-          } else if (valid) {
-            float4* dst = part + c * 8 * (2 * kBM);
+              for (int i = 0; i < NV / 8; ++i)
+                dst[i] = make_uint4(pack_bf16x2(v[8 * i] * inv, v[8 * i + 1] * inv),
+                                    pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
+                                    pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
+                                    pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
+            } else if (valid) {
+              float4* dst = part + (c * 8 + mine_at / 4) * (2 * kBM);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i * (2 * kBM)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              for (int i = 0; i < NV / 4; ++i)
+                dst[i * (2 * kBM)] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+        };
+        if constexpr (F8) {
+          if (it.duo) write(std::integral_constant<int, 2>{});
+          else write(std::integral_constant<int, 1>{});
+        } else {
+          write(std::integral_constant<int, 1>{});
         }
-        if (valid && (it.two || s == 0)) {
+        if (valid && (it.two || s == 0) && !(it.duo && lane >= 16)) {
           if (whole) {
             p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] =
                 l > 0.f ? (m_ref + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
@@ -1164,7 +1221,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       e_phase ^= 1u;
       finished();
     }
-    if (threadIdx.x == 0) p.head[cta] = hd;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n" ::: "memory");
     if (warp == 8) {
@@ -1288,121 +1344,131 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nq;
           continue;
         }
-        const int steps2 = unit_count(it) >> 2;  // pairs of tiles (one row tile) or tiles (two)
-        auto halves = [&](int j) { return it.len - (it.j0 + j) * kBN > kHalf ? 2 : 1; };
+        const int rounds = rounds_of(it);
         if (warp == 9) {
           constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, kHalf, 0, 0) : idesc_bf16_f32(kBM, kHalf, 0, 0);
+          constexpr uint32_t idesc_tile = F8 ? idesc_e4m3_f32(kBM, kBN, 0, 0) : idesc_bf16_f32(kBM, kBN, 0, 0);
           auto desc = [&](uint32_t a) { return SW64 ? sdesc_sw64(a, 16, 512) : sdesc_sw128(a, 16, 1024); };
           for (int k = 0; k < (it.two ? 2 : 1) && ok; ++k)
             ok = wait(Lay::B_QFULL + ((nq + k) & 1), ((nq + k) >> 1) & 1, kSiteTQFull);
           const uint64_t dq0 = desc(sb + Lay::Q_OFF + (nq & 1) * Lay::QTILE);
           const uint64_t dq1 = it.two ? desc(sb + Lay::Q_OFF + ((nq + 1) & 1) * Lay::QTILE) : dq0;
-          // The units of both streams for one half: one round of waits, then all their products.
-          for (int v = 0; v < steps2 && ok; ++v) {
-            const int ja = it.two ? v : 2 * v, jb = it.two ? v : 2 * v + 1;
-            const uint32_t na = n_ld + ja, nb = n_ld + jb;
-            const uint32_t sa = na % NR, sbl = nb % NR;
-            const int ha = halves(ja), hb = jb < nj ? halves(jb) : 0;
-            ok = wait(Lay::B_KVFULL + sa, (na / NR) & 1u, kSiteTKvFull);
-            if (ok && !it.two && hb) ok = wait(Lay::B_KVFULL + sbl, (nb / NR) & 1u, kSiteTKvFull);
-            for (int half = 0; half < ha && ok; ++half) {  // the second tile is no fuller than the first
-              const bool b_too = half < hb;
-              const int b0 = 2 * half, b1 = b0 + 1;
-              // the buffers' last P~ have been multiplied
-              if ((used >> b0) & 1u) {
-                ok = wait(Lay::B_PVDONE + b0, (phases >> b0) & 1u, kSiteTPvDone);
-                phases ^= 1u << b0;
-              }
-              if (ok && b_too && ((used >> b1) & 1u)) {
-                ok = wait(Lay::B_PVDONE + b1, (phases >> b1) & 1u, kSiteTPvDone);
-                phases ^= 1u << b1;
-              }
-              if (!ok) break;
-              used |= (b_too ? 3u : 1u) << b0;
-              tc_fence_after();
-              const uint64_t dka = desc(sb + Lay::KV_OFF + sa * Lay::TILE + half * kHalf * Lay::ROWB);
-              const uint64_t dkb = desc(sb + Lay::KV_OFF + sbl * Lay::TILE + half * kHalf * Lay::ROWB);
-              const uint32_t tS = tmem + Lay::TM_S + 64 * b0;
-              const bool last = v == steps2 - 1 && half == ha - 1;
-              if (elect_one()) {
-                auto products = [&](uint32_t d, uint64_t dq, uint64_t dk) {
-                  constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
-#pragma unroll
-                  for (int term = 0; term < (F8 ? 2 : 1); ++term)
-#pragma unroll
-                    for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
-                      const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
-                      const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
-                      if constexpr (F8) mma_ss_f8(d, desc_add(dq, off + term * Lay::TILE), desc_add(dk, off), idesc, acc);
-                      else mma_ss(d, desc_add(dq, off), desc_add(dk, off), idesc, acc);
-                    }
-                };
-                products(tS, dq0, dka);
-                tc_commit(bar(Lay::B_SFULL + b0));
-                if (!it.two && half == ha - 1) tc_commit(bar(Lay::B_KVEMPTY + sa));
-                if (b_too) {
-                  products(tS + 64, dq1, dkb);
-                  tc_commit(bar(Lay::B_SFULL + b1));
-                  if (half == hb - 1) tc_commit(bar(Lay::B_KVEMPTY + sbl));
-                }
-                if (last) {  // q is free after the item's last S
-                  tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
-                  if (it.two) tc_commit(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
-                }
-              }
-              __syncwarp();
+          // A round: one set of waits, then the products of both streams.
+          for (int v = 0; v < rounds && ok; ++v) {
+            const Unit u0 = unit_at(it, v, 0), u1 = unit_at(it, v, 1);
+            if (!u0.live) continue;
+            const uint32_t n = n_ld + u0.j, slot = n % NR;
+            const bool full = full_tile(it, u0.j);
+            if (u0.half == 0) ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
+            const int b0 = 2 * (v & 1), b1 = b0 + 1;
+            // the buffers' last P~ have been multiplied
+            if (ok && ((used >> b0) & 1u)) {
+              ok = wait(Lay::B_PVDONE + b0, (phases >> b0) & 1u, kSiteTPvDone);
+              phases ^= 1u << b0;
             }
+            if (ok && u1.live && ((used >> b1) & 1u)) {
+              ok = wait(Lay::B_PVDONE + b1, (phases >> b1) & 1u, kSiteTPvDone);
+              phases ^= 1u << b1;
+            }
+            if (!ok) break;
+            used |= (u1.live ? 3u : 1u) << b0;
+            tc_fence_after();
+            const uint32_t kbase = sb + Lay::KV_OFF + slot * Lay::TILE;
+            const uint64_t dk0 = desc(kbase + u0.half * kHalf * Lay::ROWB), dk1 = desc(kbase + u1.half * kHalf * Lay::ROWB);
+            const uint32_t tS = tmem + Lay::TM_S + 64 * b0;
+            const bool tile_ends = !it.two || u0.half == 1 || !full;
+            if (elect_one()) {
+              auto products = [&](uint32_t d, uint64_t dq, uint64_t dk, uint32_t shape, auto terms) {
+                constexpr int PER = Lay::ROWB / 32;  // K steps of a chunk
+#pragma unroll
+                for (int term = 0; term < decltype(terms)::value; ++term) {
+#pragma unroll
+                  for (int kk = 0; kk < D / Lay::KSTEP; ++kk) {
+                    const uint32_t off = (kk / PER) * Lay::CHUNK + (kk % PER) * 32;
+                    const uint32_t acc = (term > 0 || kk > 0) ? 1u : 0u;
+                    if constexpr (F8) mma_ss_f8(d, desc_add(dq, off + term * Lay::TILE), desc_add(dk, off), shape, acc);
+                    else mma_ss(d, desc_add(dq, off), desc_add(dk, off), shape, acc);
+                  }
+                }
+              };
+              // One row tile: both units' S are the product with the whole tile, which reads q once
+              // (63 cycles a step for 128 keys, 2 x 48 for two halves).
+              constexpr std::integral_constant<int, 1> one_term{};
+              constexpr std::integral_constant<int, F8 ? 2 : 1> all_terms{};
+              if (it.two || !u1.live) {
+                if (F8 && it.duo) products(tS, dq0, dk0, idesc, one_term);
+                else products(tS, dq0, dk0, idesc, all_terms);
+                tc_commit(bar(Lay::B_SFULL + b0));
+                if (u1.live) {
+                  products(tS + 64, dq1, dk1, idesc, all_terms);
+                  tc_commit(bar(Lay::B_SFULL + b1));
+                }
+              } else {
+                if (F8 && it.duo) products(tS, dq0, dk0, idesc_tile, one_term);
+                else products(tS, dq0, dk0, idesc_tile, all_terms);
+                tc_commit(bar(Lay::B_SFULL + b0));
+                tc_commit(bar(Lay::B_SFULL + b1));
+              }
+              if (tile_ends) tc_commit(bar(Lay::B_KVEMPTY + slot));
+              if (tile_ends && u0.j == nj - 1) {  // q is free after the item's last S
+                tc_commit(bar(Lay::B_QEMPTY + (nq & 1)));
+                if (it.two) tc_commit(bar(Lay::B_QEMPTY + ((nq + 1) & 1)));
+              }
+            }
+            __syncwarp();
           }
           if (!ok) break;
         } else {
           constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
           constexpr int NK = kHalf / Lay::KSTEP;
-          for (int v = 0; v < steps2 && ok; ++v) {
-            const int ja = it.two ? v : 2 * v, jb = it.two ? v : 2 * v + 1;
-            const int ha = halves(ja), hb = jb < nj ? halves(jb) : 0;
-            for (int half = 0; half < ha && ok; ++half) {
-              for (int s = 0; s < 2; ++s) {
-                if (s == 1 && half >= hb) continue;
-                const int j = s ? jb : ja, buf = 2 * half + s;
-                const uint32_t n = n_ld + j, slot = NR + n % NR;
-                const int left = it.len - (it.j0 + j) * kBN - half * kHalf;  // keys of the half inside the sequence, or more
-                const int steps = min(NK, ceil_div(left, Lay::KSTEP));
-                if (!it.two || s == 0) {
-                  if (half == 0) {
-                    ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
-                    if (!ok) break;
-                  }
-                  clear_rows(slot, half * kHalf + left, half * kHalf + steps * Lay::KSTEP);
-                }
-                ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
+          for (int v = 0; v < rounds && ok; ++v) {
+            for (int s = 0; s < 2; ++s) {
+              const Unit un = unit_at(it, v, s);
+              if (!un.live) continue;
+              const int buf = 2 * (v & 1) + s;
+              const uint32_t n = n_ld + un.j, slot = NR + n % NR;
+              const bool full = full_tile(it, un.j);
+              const int left = it.len - (it.j0 + un.j) * kBN - un.half * kHalf;  // keys of the half inside the sequence, or more
+              const int steps = min(NK, ceil_div(left, Lay::KSTEP));
+              if (s == 0 && un.half == 0) {
+                ok = wait(Lay::B_KVFULL + slot, (n / NR) & 1u, kSiteTKvFull);
                 if (!ok) break;
-                phases ^= 1u << buf;
-                tc_fence_after();
-                const uint32_t tP = tmem + Lay::TM_S + 64 * buf, tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
-                const uint32_t more = (v > 0 || half > 0) ? 1u : 0u;  // not the stream's first product
-                const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE + half * kHalf * Lay::ROWB;
-                const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
-                const bool tile_ends = half == (s ? hb : ha) - 1 && (!it.two || s == 1);
-                const bool last = v == steps2 - 1 && half == ha - 1 && (s == 1 || half >= hb);
-                if (elect_one()) {
-#pragma unroll
-                  for (int kk = 0; kk < NK; ++kk) {
-                    if (kk >= steps) continue;
-                    const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
-                    const uint32_t acc = kk > 0 ? 1u : more;
-                    if constexpr (F8) {
-                      mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
-                      mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
-                    } else {
-                      mma_ts(tO, tP + kk * 8, dv, idesc, acc);
-                    }
-                  }
-                  tc_commit(bar(Lay::B_PVDONE + buf));
-                  if (tile_ends) tc_commit(bar(Lay::B_KVEMPTY + slot));
-                  if (last) tc_commit(bar(Lay::B_OFULL));
-                }
-                __syncwarp();
               }
+              if (!it.two || s == 0) clear_rows(slot, un.half * kHalf + left, un.half * kHalf + steps * Lay::KSTEP);
+              ok = wait(Lay::B_PFULL + buf, (phases >> buf) & 1u, kSiteTPFull);
+              if (!ok) break;
+              phases ^= 1u << buf;
+              tc_fence_after();
+              const uint32_t tP = tmem + Lay::TM_S + 64 * buf, tO = tmem + (s ? Lay::TM_O1 : Lay::TM_O0);
+              const uint32_t more = v > 0 ? 1u : 0u;  // not the stream's first product
+              const uint32_t vbase = sb + Lay::KV_OFF + slot * Lay::TILE + un.half * kHalf * Lay::ROWB;
+              const uint64_t dv0 = SW64 ? sdesc_sw64(vbase, Lay::CHUNK, 512) : sdesc_sw128(vbase, Lay::CHUNK, 1024);
+              const bool tile_ends = it.two ? s == 1 && (un.half == 1 || !full) : s == 1 || !full;
+              if (elect_one()) {
+                auto product = [&](int kk, auto terms) {
+                  const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
+                  const uint32_t acc = kk > 0 ? 1u : more;
+                  if constexpr (F8) {
+                    mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
+                    if constexpr (decltype(terms)::value == 2) mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
+                  } else {
+                    mma_ts(tO, tP + kk * 8, dv, idesc, acc);
+                  }
+                };
+                if (F8 && it.duo) {
+#pragma unroll
+                  for (int kk = 0; kk < NK; ++kk)
+                    if (kk < steps) product(kk, std::integral_constant<int, 1>{});
+                } else {
+#pragma unroll
+                  for (int kk = 0; kk < NK; ++kk)
+                    if (kk < steps) product(kk, std::integral_constant<int, 2>{});
+                }
+                tc_commit(bar(Lay::B_PVDONE + buf));
+                if (tile_ends) tc_commit(bar(Lay::B_KVEMPTY + slot));
+                if (tile_ends && un.j == nj - 1) tc_commit(bar(Lay::B_OFULL));
+              }
+              __syncwarp();
             }
           }
           if (!ok) break;

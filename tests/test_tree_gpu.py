@@ -155,6 +155,19 @@ def test_chains(dtype, d, G):
     verify(c, q, cu, None, o, lse)
 
 
+@pytest.mark.parametrize("dtype,d", KINDS)
+@pytest.mark.parametrize("G,n", [(1, 33), (1, 64), (3, 21), (5, 8), (8, 8), (16, 3), (33, 1), (64, 1)])
+@pytest.mark.parametrize("masked", [False, True])
+def test_rows_of_half_a_tile(dtype, d, G, n, masked):
+    """33 to 64 rows, contexts that end before and behind the middle of a key tile."""
+    ctx = [0, 1, 20, 63, 64, 65, 100, 128, 190, 700, 2100]
+    drafted = [n] * len(ctx)
+    c = build(ctx, drafted, 2, d, 64, dtype, seed=d + G)
+    mask = tree_mask(drafted, seed=n, empty=0.2) if masked else None
+    q, cu, o, lse = run(c, drafted, 2 * G, mask)
+    verify(c, q, cu, mask, o, lse)
+
+
 def test_rows_that_see_nothing():
     drafted = [4, 2]
     c = build([0, 0], drafted, 1)
