@@ -38,7 +38,7 @@
 //
 // Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
 // 64 ragged contexts of 512 to 8192, one token, bf16: 146 (86%).  Two contexts of 131072, 64 rows,
-// E4M3: 140 (56%; the softmax with its conversions bounds it).  A call of little work costs
+// E4M3: 138 (57%; the softmax with its conversions bounds it).  A call of little work costs
 // 11 to 13: two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -71,7 +71,7 @@ __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8
 // as one row tile, where every row has a thread and its reference stays in a register.
 constexpr int kSwapped = 32;
 // E4M3 items above that and up to 64 rows: see Seg::duo.  Measured (two contexts of 131072, 64 rows,
-// us): 158 with both terms as products of their own, 140.
+// us): 158 with both terms as products of their own, 138.
 constexpr int kDuo = 64;
 constexpr int kMinPart = 4;  // no CTA takes less of the list: the longest tile
 
@@ -985,8 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_x64(t_s, sa);
           } else {
             uint32_t lo[NC];
-            tmem_ld_duo(t_s, sa);
-            tmem_ld_duo(t_s + kLoLanes, lo);
+            tmem_ld_duo_both(t_s, sa, lo);
 #pragma unroll
             for (int c = 0; c < NC; ++c) sa[c] = __float_as_uint(__uint_as_float(sa[c]) + __uint_as_float(lo[c]));
           }
