@@ -346,7 +346,12 @@ __device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu
       const int32_t* row = path + static_cast<int64_t>(b) * width;
       for (int i = threadIdx.x; i < k.count; i += blockDim.x) {
         const int p = __ldg(row + i);
-        if (p >= n || p <= (i ? __ldg(row + i - 1) : -1)) bad = kSitePath;
+        if (p >= n || p <= (i ? __ldg(row + i - 1) : -1)) {
+          bad = kSitePath;
+        } else if (p != i) {  // a token moves here: no other slot may hold the page
+          const int page = __ldcg(c.page_table + static_cast<int64_t>(k.slot) * c.max_pages + (k.base + i) / c.page_size);
+          if (page < 0 || page >= c.pages || __ldcg(c.refs + page) != 1) bad = kSitePage;
+        }
       }
     }
     for (int j = threadIdx.x; slots && j < b; j += blockDim.x)

@@ -69,6 +69,7 @@ ATTN_API attn_status_t attn_rope(const attn_rope_plan_t* plan, int inverse, attn
  * refs[page] counts the slots that hold a page; 0 means free.  A slot of lens[s]
  * tokens holds exactly ceil(lens[s] / page_size) pages; entries behind those are not
  * read.  A page that is not full is held by one slot only (attn_cache_fork copies it).
+ * Tokens in a shared page are shared: fork a slot when its tokens have been appended.
  * page_size: a power of two from 16 to 1024; d 64 or 128; slots <= 8192.
  * Page operations (alloc, free, fork, copy, compact) that share a cache must not run
  * at the same time: issue them on one stream. */
@@ -124,8 +125,9 @@ ATTN_API attn_status_t attn_cache_copy(const attn_cache_t* cache, const int32_t*
  * cu_q[b] tokens of slot slots[b] (NULL: slot b) are drafted; path[b][0..accepted[b])
  * names, strictly increasing, which of them stay.  In every layer they move together
  * behind the context, lens becomes context + accepted[b], and pages behind the new end
- * lose a reference.  A sequence whose path is not valid is left alone, error recorded,
- * and so is the second of two sequences with the same slot.  B <= 1024.
+ * lose a reference.  A sequence whose path is not valid, or whose tokens would move into a
+ * page that another slot holds too, is left alone, error recorded, and so is the second
+ * of two sequences with the same slot.  B <= 1024.
  */
 ATTN_API attn_status_t attn_cache_compact(const attn_cache_t* cache, const int32_t* cu_q,
                                           const int32_t* path, int path_width,

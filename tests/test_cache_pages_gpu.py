@@ -133,6 +133,59 @@ def test_refused_requests_leave_the_rest():
     ea.get_device_status()
 
 
+def test_compact_leaves_shared_pages_alone():
+    """Drafted tokens in a full page that a fork shares: nothing moves; kept in place, they may stay."""
+    p = Pair(4, 4, 16, 16)
+    p.alloc([0, 1], [32, 20])
+    p.fork([0], [2])
+    p.c.compact(ints([0, 6, 9]), ints([[2, 4], [1, -1]]), ints([2, 1]), slots=ints([0, 1]))
+    p.b.compact([0, 0, 3], [[-1], [1]], [0, 1], [0, 1])  # slot 1's token moves in its own page
+    p.same()
+    with pytest.raises(ea.AttnError):
+        ea.get_device_status()
+    p.compact([6], [[0, 1, 2]], [2])
+    p.same()
+    ea.get_device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float8_e4m3fn])
+def test_offsets_beyond_31_bits(dtype):
+    """Pages whose first value has an index above 2^31, and above 2^32 in bytes, in the second layer."""
+    layers, pages, page, heads, d = 2, 70000, 16, 8, 128
+    c = ea.KVCache.empty(layers, pages, page, heads, d, 4, 8, dtype=dtype)
+    assert c.k[1, -40:].storage_offset() > 2 ** 31
+    c.refs[:-40] = 1
+    lens = [50, 33, 128]
+    assert c.alloc(ints([0, 1, 2]), ints(lens)).tolist() == [1, 1, 1]
+    assert c.page_table[:3].max() >= pages - 40 and c.page_table[0].tolist()[:4] == list(range(pages - 40, pages - 36))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    T = sum(lens)
+    k, v = (torch.randn((T, heads, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((T, heads, d), generator=g, device="cuda").to(torch.bfloat16)
+    cu = ints([0, 50, 83, 211])
+    for layer in range(layers):
+        ea.rope_append(c, None, k, v, cu, layer=layer)
+    assert torch.equal(c.k[1, pages - 40].view(torch.uint8), k[:16].to(dtype).view(torch.uint8))
+    o, lse = ea.tree_fwd(c, q, cu, layer=1)
+    small = ea.KVCache.empty(1, 16, page, heads, d, 4, 8, dtype=dtype)
+    small.alloc(ints([0, 1, 2]), ints(lens))
+    ea.rope_append(small, None, k, v, cu)
+    want = ea.tree_fwd(small, q, cu)
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    # token 45 of slot 0 takes the place of token 40, then a fork copies the tail
+    c.compact(ints([0, 10]), ints([[5]]), ints([1]), slots=ints([0]))
+    assert c.fork(ints([0]), ints([3])).tolist() == [1]
+    assert c.lens.tolist() == [41, 33, 128, 41]
+    for t, x in ((c.k, k), (c.v, v)):
+        for s in (0, 3):
+            got = t[1, int(c.page_table[s, 2])].view(torch.uint8)
+            rows = x[list(range(32, 40)) + [45]].to(dtype).view(torch.uint8)
+            assert torch.equal(got[:9], rows)
+    c.copy(ints([int(c.page_table[0, 0])]), ints([pages - 1]))
+    assert torch.equal(c.v[1, pages - 1].view(torch.uint8), v[:16].to(dtype).view(torch.uint8))
+    ea.get_device_status()
+
+
 def test_compact_defaults_to_the_first_slots():
     p = Pair(3, 4, 16, 16)
     p.alloc([0, 1, 2], [20, 33, 5])

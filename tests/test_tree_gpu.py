@@ -259,6 +259,28 @@ def test_long_batches_of_single_tokens(dtype, d):
     verify(c, q, cu, None, o, lse)
 
 
+@pytest.mark.parametrize("dtype", list(SCALES))
+def test_1024_sequences(dtype):
+    """As many sequences as a batch holds, some of them without a token."""
+    r = random.Random(3)
+    drafted = [r.choice([0, 1, 1, 2, 7]) for _ in range(1024)]
+    ctx = [r.randint(0, 90) for _ in drafted]
+    c = build(ctx, drafted, 1, 64, 16, dtype, seed=13)
+    q, cu, o, lse = run(c, drafted, 4)
+    verify(c, q, cu, None, o, lse)
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 2, 6], [0, 3, 6, 7], [-1, 2, 4, 6]])
+def test_offsets_that_decrease_or_leave_the_batch(cu):
+    c = build([20, 5, 9], [3, 3, 3], 1, 64, 16)
+    q = torch.randn(6, 2, 64, device="cuda").to(torch.bfloat16)
+    o, lse = torch.full_like(q, 7.0), torch.full((2, 6), 7.0, device="cuda")
+    ea.tree_fwd(c, q, ints(cu), out=o, lse=lse)
+    assert (o == 7).all() and (lse == 7).all()
+    with pytest.raises(ea.AttnError):
+        ea.get_device_status()
+
+
 def test_rows_outside_the_batch_stay():
     c = build([100, 30], [3, 2], 1, 128, 16)
     q = torch.randn(12, 2, 128, device="cuda").to(torch.bfloat16)
@@ -336,6 +358,67 @@ def test_repeatable_on_streams_and_in_graphs():
             graphs[i].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(want[0], x) and torch.equal(want[1], y) for x, y in held)
+    ea.get_device_status()
+
+
+def test_a_step_in_a_graph():
+    """Pages, append, attention and compaction of a decoding step, captured once and replayed on
+    another stream: every replay continues from the state that the last one left."""
+    heads, G, d, page, n = 2, 4, 64, 16, 6
+    plan = ea.Rope(d)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    start = [37, 16, 90]
+    T = n * len(start)
+    q, k, v = (torch.randn((T, h, d), generator=g, device="cuda").to(torch.bfloat16) for h in (heads * G, heads, heads))
+    cu, slots = ints([n * i for i in range(len(start) + 1)]), ints([2, 0, 1])
+    mask = tree_mask([n] * len(start), 6)
+    path, took = ints([[0, 2, 5], [1, -1, -1], [-1, -1, -1]]), ints([3, 1, 0])
+    other = ints([4])
+
+    def fresh():
+        g = torch.Generator(device="cuda").manual_seed(7)
+        c = ea.KVCache.empty(1, 60, page, heads, d, 5, 12)
+        for x in (c.k, c.v):
+            x.copy_(torch.randn(x.shape, generator=g, device="cuda").to(torch.bfloat16))
+        c.alloc(ints([0, 1, 2]), ints(start))
+        c.fork(ints([0]), other)
+        return c, ints([0] * 3)
+
+    def step(c, want):
+        want.copy_(c.lens[slots.long()] + n)
+        granted = c.alloc(slots, want)
+        turned = ea.rope_append(c, q, k, v, cu, plan=plan, slots=slots)
+        o, lse = ea.tree_fwd(c, turned, cu, mask=mask, slots=slots)
+        c.compact(cu, path, took, slots=slots)
+        c.free(other)
+        fork = c.fork(ints_at(slots, 1), other)
+        return granted, turned, o, lse, fork
+
+    def ints_at(t, i):
+        return t[i:i + 1]
+
+    eager, want = fresh()
+    seen = []
+    for _ in range(4):
+        seen.append([x.clone() for x in step(eager, want)] + [x.clone() for x in (eager.lens, eager.refs)])
+    c, want = fresh()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    keep = [x.clone() for x in (c.page_table, c.lens, c.refs, c.k, c.v)]
+    step(c, want)  # once outside, then back
+    for x, y in zip((c.page_table, c.lens, c.refs, c.k, c.v), keep):
+        x.copy_(y)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = step(c, want)
+    s = torch.cuda.Stream()
+    for i in range(4):
+        with torch.cuda.stream(s):
+            graph.replay()
+        s.synchronize()
+        for x, y in zip(list(out) + [c.lens, c.refs], seen[i]):
+            assert torch.equal(x, y)
+    assert torch.equal(c.k, eager.k) and torch.equal(c.v, eager.v)
     ea.get_device_status()
 
 
