@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -48,9 +49,12 @@ class CacheView(ctypes.Structure):
                 ("e4m3", ctypes.c_int), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
-_TwoRows, _ThreeRows = Rows * 2, Rows * 3
-_ROW = ctypes.sizeof(Rows)
-_at = ctypes.byref
+# `Rows` structs, passed as bytes written in one step: two addresses, the heads, six strides.
+_one_row = "PPi4x6q"
+assert struct.calcsize(_one_row) == ctypes.sizeof(Rows)
+_row, _two_rows = struct.Struct(_one_row).pack, struct.Struct(2 * _one_row).pack
+_no_row = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+_Tensor, _int32, _bf16 = torch.Tensor, torch.int32, torch.bfloat16
 
 
 def declare(lib) -> None:
@@ -101,9 +105,9 @@ def _on(dev: torch.device, f, *args) -> None:
 
 def _list(t, name: str, dev: torch.device, n: Optional[int] = None) -> int:
     """The address of a contiguous int32 list on `dev`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32:
+    if not isinstance(t, _Tensor) or t.dtype is not _int32:
         raise ValueError(f"{name} must be an int32 tensor")
-    if t.device != dev:
+    if t.get_device() != dev.index:
         raise ValueError(f"{name} must be on {dev}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -118,20 +122,27 @@ def _cuda(t, name: str):
 
 
 def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
-    """The six strides of a tensor's rows and of its result's (y None: it has none), checked:
-    [*lead, H, d] with contiguous heads."""
-    if y is None:
-        y = x
-    for t, what in ((x, name), (y, "out of " + name)):
-        if t.dtype is not dtype or t.device != dev:
-            raise ValueError(f"{what} must be {dtype} on {dev}")
-    if y is not x and y.shape != shape:
-        raise ValueError(f"out of {name} has the wrong shape")
+    """One entry of the library's row descriptions, checked: tensor, result (None: it has
+    none), heads and the six strides of [*lead, H, d] with contiguous heads."""
+    if x.dtype is not dtype or x.get_device() != dev.index:
+        raise ValueError(f"{name} must be {dtype} on {dev}")
     sx = x.stride()
-    sy = sx if y is x else y.stride()
-    if (sx[-1] != 1 or sy[-1] != 1) and x.numel():
+    if sx[-1] != 1 and x.numel():
         raise ValueError(f"the values of a head of {name} must be contiguous")
-    return (sx[0] if batch else 0, sx[-3], sx[-2], sy[0] if batch else 0, sy[-3], sy[-2])
+    bx, tx, hx = sx[0] if batch else 0, sx[-3], sx[-2]
+    if y is None:
+        return x.data_ptr(), 0, shape[-2], bx, tx, hx, bx, tx, hx
+    if y is x:
+        at = x.data_ptr()
+        return at, at, shape[-2], bx, tx, hx, bx, tx, hx
+    if y.dtype is not dtype or y.get_device() != dev.index:
+        raise ValueError(f"out of {name} must be {dtype} on {dev}")
+    if y.shape != shape:
+        raise ValueError(f"out of {name} has the wrong shape")
+    sy = y.stride()
+    if sy[-1] != 1 and y.numel():
+        raise ValueError(f"the values of a head of out of {name} must be contiguous")
+    return (x.data_ptr(), y.data_ptr(), shape[-2], bx, tx, hx, sy[0] if batch else 0, sy[-3], sy[-2])
 
 
 class Rope:
@@ -220,12 +231,9 @@ def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
         _cuda(q_out, "out of q")
         if k is not None:
             _cuda(k_out, "out of k")
-    rows = _TwoRows()
-    rows[0] = (q.data_ptr(), q_out.data_ptr(), shape[-2],
-               *_rows(q, q_out, "q", dtype, dev, shape, not packed))
-    if k is not None:
-        rows[1] = (k.data_ptr(), k_out.data_ptr(), k_shape[-2],
-                   *_rows(k, k_out, "k", dtype, dev, k_shape, not packed))
+    batch = not packed
+    rows = _two_rows(*_rows(q, q_out, "q", dtype, dev, shape, batch),
+                     *(_no_row if k is None else _rows(k, k_out, "k", dtype, dev, k_shape, batch)))
     if packed:
         cu = _list(cu_seqlens, "cu_seqlens", dev)
         B, tokens = cu_seqlens.numel() - 1, shape[0]
@@ -400,15 +408,13 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
     ``positions`` (int32 ``[T]``; default: the token's place in the cache).  Returns the rotated q
     (``out``; q itself is allowed), or None without q."""
     lib = _lib_of()
-    dev, bf16 = cache.device, torch.bfloat16
+    dev = cache.device
     _cuda(k, "k")
     _cuda(v, "v")
     T, _, d = shape = k.shape if k.dim() == 3 else (0, 0, 0)
     if d != cache.d or v.shape != shape:
         raise ValueError(f"k and v must be [T, heads, {cache.d}]")
-    rows, made = _ThreeRows(), None
-    rows[1] = (k.data_ptr(), None, shape[1], *_rows(k, None, "k", bf16, dev, shape, False))
-    rows[2] = (v.data_ptr(), None, shape[1], *_rows(v, None, "v", bf16, dev, shape, False))
+    made = q_row = None
     if q is not None:
         _cuda(q, "q")
         q_shape = q.shape
@@ -418,14 +424,15 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
             out = made = torch.empty_like(q, memory_format=torch.contiguous_format)
         else:
             _cuda(out, "out")
-        rows[0] = (q.data_ptr(), out.data_ptr(), q_shape[1],
-                   *_rows(q, out, "q", bf16, dev, q_shape, False))
+        q_row = _row(*_rows(q, out, "q", _bf16, dev, q_shape, False))
+    k_row = _row(*_rows(k, None, "k", _bf16, dev, shape, False))
+    v_row = _row(*_rows(v, None, "v", _bf16, dev, shape, False))
     if plan is not None and plan.turns.device != dev:
         raise ValueError(f"the plan must be on {dev}")
     cu = _list(cu_q, "cu_q", dev)
     B = cu_q.numel() - 1
     _on(dev, lib.attn_rope_append, cache._ref, layer, None if plan is None else plan._ref,
-        None if q is None else _at(rows, 0), _at(rows, _ROW), _at(rows, 2 * _ROW), B, T, cu,
+        q_row, k_row, v_row, B, T, cu,
         None if slots is None else _list(slots, "slots", dev, B),
         None if positions is None else _list(positions, "positions", dev, T),
         _stream(dev, stream, made))

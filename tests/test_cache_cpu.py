@@ -82,7 +82,7 @@ def test_page_operations_refuse(lib):
 
 def test_rope_refuses(lib):
     def call(p=plan(), type=0, t=(rows(), rows()), count=2, d=128, B=1, N=4, cu=None, pos=None):
-        two = ec._TwoRows(*t)
+        two = (ec.Rows * 2)(*t)
         return lib.attn_rope(None if p is None else ctypes.byref(p), 0, type, two, count, d, B, N, cu, pos, None)
     assert call(p=None) == BAD and call(p=plan(turns=None)) == BAD and call(p=plan(turns=FAKE + 4)) == BAD
     assert call(p=plan(dim=24)) == NO and call(p=plan(dim=256)) == NO and call(p=plan(dim=0)) == NO
