@@ -37,8 +37,8 @@
 // copies and products, frees TMEM and returns.
 //
 // Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
-// 64 ragged contexts of 512 to 8192, one token, bf16: 146 (86%).  Two contexts of 131072, 64 rows,
-// E4M3: 138 (57%; the softmax with its conversions bounds it).  A call of little work costs
+// 64 ragged contexts of 512 to 8192, one token, bf16: 144 (86%).  Two contexts of 131072, 64 rows,
+// E4M3: 133 (59%; the softmax with its conversions bounds it).  A call of little work costs
 // 11 to 13: two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -73,7 +73,7 @@ constexpr int kSwapped = 32;
 // E4M3 items above that and up to 64 rows: see Seg::duo.  Measured (two contexts of 131072, 64 rows,
 // us): 158 with both terms as products of their own, 138.
 constexpr int kDuo = 64;
-constexpr int kMinPart = 4;  // no CTA takes less of the list: the longest tile
+constexpr int kMinPart = 7;  // no CTA takes less of the list: the longest tile
 
 struct TreeParams {
   __nv_bfloat16* o;
@@ -132,9 +132,12 @@ struct Layout {
                        B_KVFULL = 31, B_KVEMPTY = B_KVFULL + NSTAGE, NBARS = B_KVEMPTY + NSTAGE;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;
   static constexpr int TABLE_OFF = MISC_OFF + 128;
-  // Cost of a key tile with one and with two row tiles (the copies bound the first, the softmax of
-  // 256 rows the second), and of beginning an item.
-  static constexpr int COST_ONE = 2, COST_PAIR = ESZ * D == 256 ? 3 : 4, COST_ITEM = ESZ * D == 256 ? 7 : 12;
+  // Cost of a key tile with one and with two row tiles, and of beginning an item (its mask, queries
+  // and epilogue), in units of about 1000 to 1300 cycles, as homogeneous batches and then mixed ones
+  // measured: 16 trees of 48 tokens, bf16, 121 us with 2, 3, 7 and 114 with 4, 7, 24; 64 single tokens,
+  // E4M3, 124 with an item at 12 and 113 at 24.
+  static constexpr int COST_ONE = !F8 && D == 128 ? 4 : 2, COST_PAIR = !F8 && D == 128 ? 7 : 4,
+                       COST_ITEM = F8 || D == 128 ? 24 : 12;
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -1629,7 +1632,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   // describe.
   const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
   const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
-  if (items > INT32_MAX / (4 * tiles + 12)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 4
+  if (items > INT32_MAX / (7 * tiles + 24)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 7, an item 24
   int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
   if (grid > kMaxGrid) grid = kMaxGrid;
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;
