@@ -445,80 +445,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // E4M3: softmax warp w writes its eighth of an item's queries, from q slot nq on: each row is
   // scaled by the power of two that brings its largest value into [128, 256), hi = E4M3(x), lo =
-  // E4M3(x - hi).
+  // E4M3(x - hi).  A row is held by D / 8 lanes, 8 values each.  Eight rows' loads are in flight: they
+  // queue behind the copies of K and V, which have begun.  The loop is not unrolled, as its code runs
+  // cold at the head of an item, where fetching it is what counts.
   auto split_q = [&](const Seg& it, int nq, int w8) -> bool {
     float* qs = reinterpret_cast<float*>(smem + Lay::QS_OFF);
-    for (int k = 0; k < (it.two ? 2 : 1); ++k, ++nq) {
-      const int slot = nq & 1;
-      if (nq >= 2 && !wait(Lay::B_QEMPTY + slot, ((nq >> 1) - 1) & 1, kSiteTQEmpty)) return false;
-      const int rows = (it.two ? (k ? it.nt - p.tpt : p.tpt) : it.nt) * p.G;
-      const int64_t tok = it.q0 + it.tok0 + k * p.tpt;
-      uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
-      // A row is held by D / 8 lanes, 8 values each.  Four rows' loads are in flight; the loop is not
-      // unrolled, as its code runs cold at the head of an item, where fetching it is what counts.
-      constexpr int L = D / 8, R = 32 / L, U = 4;
-      const int c = lane % L;
-      auto fetch = [&](int r) {
-        const int t = r / p.G;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < rows) w = __ldcg(reinterpret_cast<const uint4*>(p.q + ((tok + t) * p.Hq + it.h * p.G + (r - t * p.G)) * D) + c);
-        return w;
-      };
-      int r = w8 * R + lane / L;
-      uint4 w[U];
+    constexpr int L = D / 8, R = 32 / L, U = 8;
+    const int c = lane % L, rows = it.nt * p.G, tile_rows = p.tpt * p.G;
+    const __nv_bfloat16* q = p.q + (static_cast<int64_t>(it.q0 + it.tok0) * p.Hq + it.h * p.G) * D + 8 * c;
+    auto fetch = [&](int r) {
+      const int t = r / p.G;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (r < rows) w = __ldcg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(t) * (p.Hq - p.G) + r) * D));
+      return w;
+    };
+    int r = w8 * R + lane / L;
+    uint4 w[U];
 #pragma unroll
-      for (int i = 0; i < U; ++i) w[i] = fetch(r + 8 * R * i);
+    for (int i = 0; i < U; ++i) w[i] = fetch(r + 8 * R * i);
+    for (int k = 0; k < (it.two ? 2 : 1); ++k)
+      if (nq + k >= 2 && !wait(Lay::B_QEMPTY + ((nq + k) & 1), (((nq + k) >> 1) - 1) & 1, kSiteTQEmpty)) return false;
 #pragma unroll 1
-      for (; __any_sync(0xffffffffu, r < rows); r += 8 * R) {
-        const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    for (; __any_sync(0xffffffffu, r < rows); r += 8 * R) {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-        for (int i = 0; i + 1 < U; ++i) w[i] = w[i + 1];
-        w[U - 1] = fetch(r + 8 * R * U);
-        float v[8];
-        float top = 0.f;
+      for (int i = 0; i + 1 < U; ++i) w[i] = w[i + 1];
+      w[U - 1] = fetch(r + 8 * R * U);
+      float v[8];
+      float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[2 * e] = __uint_as_float(u[e] << 16);
-          v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-          top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
-        }
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(u[e] << 16);
+        v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+        top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+      }
 #pragma unroll
-        for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        e = max(-100, min(e, 120));
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-        uint32_t hi[2], lo[2];
+      for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
+      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+      e = max(-100, min(e, 120));
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+      uint32_t hi[2], lo[2];
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          hi[y] = lo[y] = 0;
+      for (int y = 0; y < 2; ++y) {
+        hi[y] = lo[y] = 0;
 #pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
-            float ha, hb;
-            upper4_x2(ha, hb, a, b);
-            hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
-            lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
-          }
-        }
-        if (r < rows) {
-          if (c == 0)
-            qs[slot * kBM + r] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-          // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
-          // lo rows follow its hi rows: both are columns of one product.
-          auto at = [&](int row) {
-            return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
-                                    : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
-          };
-          const int row = it.duo ? 32 * (r >> 4) + (r & 15) : r;
-          uint8_t* lo_at = it.swapped ? base + at(r + swapped_rows(rows)) : it.duo ? base + at(row + 16) : base + Lay::TILE + at(r);
-          *reinterpret_cast<uint2*>(base + at(row)) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
+        for (int z = 0; z < 2; ++z) {
+          const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
+          float ha, hb;
+          upper4_x2(ha, hb, a, b);
+          hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
+          lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Lay::B_QFULL + slot));
+      if (r < rows) {
+        const int tile = r >= tile_rows, rt = r - tile * tile_rows, slot = (nq + tile) & 1;
+        uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
+        if (c == 0)
+          qs[slot * kBM + rt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+        // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
+        // lo rows follow its hi rows: both are columns of one product.
+        auto at = [&](int row) {
+          return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
+                                  : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
+        };
+        const int row = it.duo ? 32 * (rt >> 4) + (rt & 15) : rt;
+        uint8_t* lo_at = it.swapped ? base + at(rt + swapped_rows(rows)) : it.duo ? base + at(row + 16) : base + Lay::TILE + at(rt);
+        *reinterpret_cast<uint2*>(base + at(row)) = make_uint2(hi[0], hi[1]);
+        *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bar(Lay::B_QFULL + (nq & 1)));
+      if (it.two) mbar_arrive(bar(Lay::B_QFULL + ((nq + 1) & 1)));
     }
     return true;
   };
