@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lines = (p.max_pages + 31) >> 5;
     const int b = static_cast<int>(threadIdx.x) / lines;
     if (b < p.B) {
-      const int slot = p.slots ? __ldg(p.slots + b) : b;
+      const int slot = p.slots ? __ldcg(p.slots + b) : b;
       if (slot >= 0 && slot < p.nslots)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(p.page_table + static_cast<int64_t>(slot) * p.max_pages +
                                                       32 * (static_cast<int>(threadIdx.x) - b * lines)));
@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int b0 = min(static_cast<int>(threadIdx.x) * per, p.B), b1 = min(b0 + per, p.B);
     int sum = 0, broken = 0;
     for (int b = b0; b < b1; ++b) {
-      const int first = __ldg(p.cu + b), n = __ldg(p.cu + b + 1) - first;
-      const int slot = p.slots ? __ldg(p.slots + b) : b;
+      const int first = __ldcg(p.cu + b), n = __ldcg(p.cu + b + 1) - first;
+      const int slot = p.slots ? __ldcg(p.slots + b) : b;
       int len = 0, work = 0;
       if (n < 0 || first < 0 || n > p.T - first) {
         broken = 1;  // nothing of the batch can be told apart
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
       t_cum[0] = 0;
-      t_cu[p.B] = __ldg(p.cu + p.B);
+      t_cu[p.B] = __ldcg(p.cu + p.B);
     }
     int incl = sum;
 #pragma unroll

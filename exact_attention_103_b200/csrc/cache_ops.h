@@ -23,10 +23,12 @@ __device__ __forceinline__ void record_invalid(int* err, int site) {
   if (err) atomicCAS(err, 0, 1 | (site << 8));
 }
 
-// The serving operators follow one another on a stream in kernels of a few microseconds. Each is
-// launched as a programmatic dependent of the kernel before it and lets the next one launch at its
-// own entry; before it touches memory it waits until the kernel before it, whatever that
-// was, has completed (and with it everything earlier on the stream).
+// The serving operators follow one another on a stream in kernels of a few microseconds.  Each is
+// launched as a programmatic dependent of the kernel before it; before it touches memory it waits
+// until that one, whatever it was, has completed (and with it everything earlier on the stream).
+// At its own entry it lets the next one launch (but for the rotary kernel, whose many
+// blocks the next one's would keep from the SMs).  What the kernel before may have written is read
+// past L1 or by plain loads, never through the read-only path.
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -42,7 +44,9 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // reported here, not by a later call
+  return e;
 }
 
 constexpr int kMaxSequences = 1024;  // of a packed batch

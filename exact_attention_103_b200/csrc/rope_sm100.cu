@@ -10,7 +10,9 @@
 //
 // Bound by HBM: every value is read once and written once.  A block takes a few whole
 // tokens, so that one table of their sines (in shared memory) serves all their heads, and
-// moves 16 values of one head per thread and step with 16-byte accesses.
+// moves 16 values of one head per thread and step with 16-byte accesses.  Measured (B200): 2 x 8192
+// tokens, 16 + 16 heads, d 128, bf16: 46.8 us, 88% of the copy rate; a packed batch of 16 sequences
+// of 512 to 16384 tokens, half of each head rotated: 196 us, 95%.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -20,9 +22,9 @@
 namespace attn {
 namespace {
 
-constexpr int kThreads = 128;        // rope
+constexpr int kThreads = 128;        // rope; 256 took 48 and 202 us for the two above
 constexpr int kAppendThreads = 256;  // append
-constexpr int kAhead = 2;            // append: rows whose loads go together
+constexpr int kAhead = 2;            // append: rows whose loads go together (1: 10.9, 3: 12.0 us for the trees)
 constexpr int kMaxTok = 16;
 constexpr int kPitch = 20;  // floats of a table chunk: 8 (cos, sin) pairs, padded so that 8
                             // neighbouring chunks read as 16-byte words meet no bank twice
@@ -195,11 +197,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     k.pos = static_cast<int>(k.n);
     if (a.positions) {
-      k.pos = __ldg(a.positions + t);
+      k.pos = __ldcg(a.positions + t);
     } else if (a.cu) {
       const int b = sequence_of(a.cu, a.B, t);
       k.live = b >= 0;
-      if (b >= 0) k.pos = t - __ldg(a.cu + b);
+      if (b >= 0) k.pos = t - __ldcg(a.cu + b);
     }
     tok[threadIdx.x] = k;
   }
@@ -235,6 +237,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // the token's row of the cache.  A step of decoding has few tokens, so what counts is the
 // chain of loads behind one another: offsets, slots and the first rows come together
 // (each block takes all offsets and slots into shared memory), then lengths, then pages.
+// The rows of all tokens are dealt evenly to one wave of blocks.  Measured: 48 single tokens of 32 +
+// 8 + 8 heads 3.8 us; 32 trees of 61 tokens into an E4M3 cache 11 us (31 MB: 4.8 at the copy
+// rate, the rest is that chain).
 template <bool F8>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ RopeArgs a, int per_block) {
   extern __shared__ float table[];
@@ -283,8 +288,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
   int r = r0 + static_cast<int>(threadIdx.x) / units;
   fetch(r);
   for (int b = threadIdx.x; b <= a.B; b += kAppendThreads) {
-    cu[b] = __ldg(a.cu + b);
-    if (b < a.B) slots[b] = a.slots ? __ldg(a.slots + b) : b;
+    cu[b] = __ldcg(a.cu + b);
+    if (b < a.B) slots[b] = a.slots ? __ldcg(a.slots + b) : b;
   }
   if (threadIdx.x < kMaxTok) again[threadIdx.x] = 0;
   __syncthreads();
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
       k.b = b;
       const int slot = slots[b];
       const int first = cu[b], n = cu[b + 1] - first;
-      if (a.positions) k.pos = __ldg(a.positions + t);
+      if (a.positions) k.pos = __ldcg(a.positions + t);
       if (slot < 0 || slot >= c.slots) {
         record_invalid(a.err, kSiteSlot);
       } else {
@@ -378,8 +383,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
   }
 }
 
-// rope: tokens of a block: enough rows for eight steps of a block, fewer when that would
-// leave SMs without a block.
+// rope: tokens of a block: enough rows for eight steps of a block (four: 207 us for the packed batch,
+// sixteen: 54 for the dense one), fewer when that would leave SMs without a block.
 int tokens_per_block(int tokens, int rows_per_token, int d, int sms) {
   const int lanes = kThreads / (d / 16);
   int per = 8 * lanes / rows_per_token;
