@@ -456,7 +456,7 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
     lib = _lib_of()
     dev, d = cache.device, cache.d
     _cuda(q, "q")
-    if q.dtype is not torch.bfloat16 or q.device != dev or not q.is_contiguous():
+    if q.dtype is not _bf16 or q.get_device() != dev.index or not q.is_contiguous():
         raise ValueError(f"q must be a contiguous bfloat16 tensor on {dev}")
     shape = q.shape
     if len(shape) != 3 or shape[2] != d:
@@ -471,7 +471,7 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
               and out.shape == shape and out.is_contiguous()):
         raise ValueError("out must be like q")
     if lse is None:
-        lse = made_l = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+        lse = made_l = torch.empty(Hq, T, dtype=torch.float32, device=dev)
     elif not (lse.is_cuda and lse.device == dev and lse.dtype is torch.float32
               and tuple(lse.shape) == (Hq, T) and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [Hq, T]")
