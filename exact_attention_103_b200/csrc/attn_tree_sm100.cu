@@ -447,82 +447,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   // E4M3: softmax warp w writes its eighth of an item's queries, from q slot nq on: each row is
   // scaled by the power of two that brings its largest value into [128, 256), hi = E4M3(x), lo =
-  // E4M3(x - hi).  A row is held by D / 8 lanes, 8 values each.  Eight rows' loads are in flight: they
-  // queue behind the copies of K and V, which have begun.  The loop is not unrolled, as its code runs
-  // cold at the head of an item, where fetching it is what counts.
-  auto split_q = [&](const Seg& it, int nq, int w8) -> bool {
-    float* qs = reinterpret_cast<float*>(smem + Lay::QS_OFF);
-    constexpr int L = D / 8, R = 32 / L, U = 8;
-    const int c = lane % L, rows = it.nt * p.G, tile_rows = p.tpt * p.G;
-    const __nv_bfloat16* q = p.q + (static_cast<int64_t>(it.q0 + it.tok0) * p.Hq + it.h * p.G) * D + 8 * c;
-    auto fetch = [&](int r) {
-      const int t = r / p.G;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (r < rows) w = __ldcg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(t) * (p.Hq - p.G) + r) * D));
-      return w;
-    };
-    int r = w8 * R + lane / L;
-    uint4 w[U];
+  // E4M3(x - hi).  A row is held by D / 8 lanes, 8 values each; a warp's rows are 8 kRows apart.
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  auto load_q = [&](const Seg& it, int r) -> uint4 {
+    const int t = r / p.G;
+    const __nv_bfloat16* q = p.q + (static_cast<int64_t>(it.q0 + it.tok0) * p.Hq + it.h * p.G) * D + 8 * (lane % kLanes);
+    if (r >= it.nt * p.G) return make_uint4(0, 0, 0, 0);
+    return __ldcg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(t) * (p.Hq - p.G) + r) * D));
+  };
+  auto split_row = [&](const Seg& it, int nq, int r, const uint4& x) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w};
+    const int c = lane % kLanes, rows = it.nt * p.G, tile_rows = p.tpt * p.G;
+    float v[8];
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < U; ++i) w[i] = fetch(r + 8 * R * i);
-    for (int k = 0; k < (it.two ? 2 : 1); ++k)
-      if (nq + k >= 2 && !wait(Lay::B_QEMPTY + ((nq + k) & 1), (((nq + k) >> 1) - 1) & 1, kSiteTQEmpty)) return false;
-#pragma unroll 1
-    for (; __any_sync(0xffffffffu, r < rows); r += 8 * R) {
-      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+    for (int e = 0; e < 4; ++e) {
+      v[2 * e] = __uint_as_float(u[e] << 16);
+      v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+      top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+    }
 #pragma unroll
-      for (int i = 0; i + 1 < U; ++i) w[i] = w[i + 1];
-      w[U - 1] = fetch(r + 8 * R * U);
-      float v[8];
-      float top = 0.f;
+    for (int o = kLanes / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
+    int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    e = max(-100, min(e, 120));
+    const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
+    uint32_t hi[2], lo[2];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[2 * e] = __uint_as_float(u[e] << 16);
-        v[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-        top = fmaxf(top, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
-      }
+    for (int y = 0; y < 2; ++y) {
+      hi[y] = lo[y] = 0;
 #pragma unroll
-      for (int o = L / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // 2^(7 - exponent of top): exact, clamped so that both it and its inverse are normal
-      int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      e = max(-100, min(e, 120));
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - e) << 23);
-      uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        hi[y] = lo[y] = 0;
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-          const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
-          float ha, hb;
-          upper4_x2(ha, hb, a, b);
-          hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
-          lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
-        }
-      }
-      if (r < rows) {
-        const int tile = r >= tile_rows, rt = r - tile * tile_rows, slot = (nq + tile) & 1;
-        uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
-        if (c == 0)
-          qs[slot * kBM + rt] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
-        // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
-        // lo rows follow its hi rows: both are columns of one product.
-        auto at = [&](int row) {
-          return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
-                                  : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
-        };
-        const int row = it.duo ? 32 * (rt >> 4) + (rt & 15) : rt;
-        uint8_t* lo_at = it.swapped ? base + at(rt + swapped_rows(rows)) : it.duo ? base + at(row + 16) : base + Lay::TILE + at(rt);
-        *reinterpret_cast<uint2*>(base + at(row)) = make_uint2(hi[0], hi[1]);
-        *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
+      for (int z = 0; z < 2; ++z) {
+        const float a = v[4 * y + 2 * z] * up, b = v[4 * y + 2 * z + 1] * up;
+        float ha, hb;
+        upper4_x2(ha, hb, a, b);
+        hi[y] |= pack_e4m3x2(ha, hb) << (16 * z);
+        lo[y] |= pack_e4m3x2(a - ha, b - hb) << (16 * z);
       }
     }
+    if (r < rows) {
+      const int tile = r >= tile_rows, rt = r - tile * tile_rows, slot = (nq + tile) & 1;
+      uint8_t* base = smem + Lay::Q_OFF + slot * Lay::QTILE;
+      if (c == 0)
+        reinterpret_cast<float*>(smem + Lay::QS_OFF)[slot * kBM + rt] =
+            p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 7 + e) << 23);
+      // 16-byte units of a row are permuted as the copies' swizzle does.  A swapped item's
+      // lo rows follow its hi rows: both are columns of one product.
+      auto at = [&](int row) {
+        return Lay::ROWB == 128 ? row * 128 + (((c >> 1) ^ (row & 7)) << 4) + (c & 1) * 8
+                                : row * 64 + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + (c & 1) * 8;
+      };
+      const int row = it.duo ? 32 * (rt >> 4) + (rt & 15) : rt;
+      uint8_t* lo_at = it.swapped ? base + at(rt + swapped_rows(rows)) : it.duo ? base + at(row + 16) : base + Lay::TILE + at(rt);
+      *reinterpret_cast<uint2*>(base + at(row)) = make_uint2(hi[0], hi[1]);
+      *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
+    }
+  };
+  auto split_done = [&](const Seg& it, int nq) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(bar(Lay::B_QFULL + (nq & 1)));
       if (it.two) mbar_arrive(bar(Lay::B_QFULL + ((nq + 1) & 1)));
     }
+  };
+  // Eight rows' loads are in flight: they queue behind the copies of K and V, which have begun.  The
+  // loop is not unrolled, as its code runs cold at the head of an item, where fetching it is what counts.
+  auto split_q = [&](const Seg& it, int nq, int w8) -> bool {
+    constexpr int U = 8;
+    int r = w8 * kRows + lane / kLanes;
+    uint4 w[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) w[i] = load_q(it, r + 8 * kRows * i);
+    for (int k = 0; k < (it.two ? 2 : 1); ++k)
+      if (nq + k >= 2 && !wait(Lay::B_QEMPTY + ((nq + k) & 1), (((nq + k) >> 1) - 1) & 1, kSiteTQEmpty)) return false;
+#pragma unroll 1
+    for (; __any_sync(0xffffffffu, r < it.nt * p.G); r += 8 * kRows) {
+      const uint4 x = w[0];
+#pragma unroll
+      for (int i = 0; i + 1 < U; ++i) w[i] = w[i + 1];
+      w[U - 1] = load_q(it, r + 8 * kRows * U);
+      split_row(it, nq, r, x);
+    }
+    split_done(it, nq);
     return true;
   };
 
@@ -641,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // only when some score exceeds its row's reference by more than tau (a vote of the four warps).
     // Unrolled for 16 or 32 rows: the code of a tile is run straight through, and fetching it
     // costs more than computing it when rows that do not exist are jumped over.
-    auto swapped_item = [&](const Seg& it, int nq_item, auto blocks) -> bool {
+    // `behind` runs when the stream's last P~ has been handed over.
+    auto swapped_item = [&](const Seg& it, int nq_item, auto blocks, auto behind) -> bool {
       constexpr int NCH = decltype(blocks)::value, N = 16 * NCH;
       const int nj = it.j1 - it.j0, rows = it.nt * p.G;
       const int key = r;
@@ -813,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(Lay::B_WPFULL + s));
         ++w_pv;
       }
+      if (!behind()) return false;
       // Row sums over the keys (lanes, then warps): a lane ends with row 32 b + lane.
 #pragma unroll
       for (int b = 0; b < (N + 31) / 32; ++b) {
@@ -910,6 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       return true;
     };
     bool ok = true;
+    [[maybe_unused]] bool split = false;  // the item's queries have been written already
     if (threadIdx.x == 0) p.head[cta] = make_int4(-1, 0, 0, 0);
     for (int x = x0; x < x1 && ok;) {
       const Seg it = list.at(x, x1);
@@ -933,7 +943,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool busy = row0 < mine * p.G;   // the warp has a valid row
       float sl = p.scale_log2;
       if constexpr (F8) {
-        ok = split_q(it, nq, warp);
+        if (!split) ok = split_q(it, nq, warp);
+        split = false;
         if (!ok) break;
         // every warp has written its rows' scales
         const int mine_q = nq + (it.two ? s : 0);
@@ -950,8 +961,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (it.swapped) {
         const int width = swapped_rows(it.nt * p.G);
-        ok = width == 16 ? swapped_item(it, nq, std::integral_constant<int, 1>{})
-                         : swapped_item(it, nq, std::integral_constant<int, 2>{});
+        // E4M3, d 128: the next item's queries load beside this one's tiles, and are written before its
+        // epilogue (the other q slot, whose rows a swapped item's P~ leaves alone).  64 single tokens
+        // over 512 to 8192: 109 -> 105 us; with d 64, whose tiles are half as long, 85 -> 94.
+        Seg nx = it;
+        uint4 w[2];
+        const int qr = warp * kRows + lane / kLanes;
+        if constexpr (F8 && D == 128) {
+          if (x < x1) nx = list.at(x, x1);
+          split = x < x1 && nx.swapped && nx.j0 < nx.j1;
+          if (split) {
+            w[0] = load_q(nx, qr);
+            w[1] = load_q(nx, qr + 8 * kRows);
+          }
+        }
+        auto behind = [&]() -> bool {
+          if constexpr (F8 && D == 128) {
+            if (split) {
+              const int n = nq + 1;
+              if (n >= 2 && !wait(Lay::B_QEMPTY + (n & 1), ((n >> 1) - 1) & 1, kSiteTQEmpty)) return false;
+#pragma unroll 1
+              for (int i = 0; i < 2; ++i) {
+                split_row(nx, n, qr + 8 * kRows * i, i ? w[1] : w[0]);
+              }
+              split_done(nx, n);
+            }
+          }
+          return true;
+        };
+        ok = width == 16 ? swapped_item(it, nq, std::integral_constant<int, 1>{}, behind)
+                         : swapped_item(it, nq, std::integral_constant<int, 2>{}, behind);
         if (!ok) break;
         ++nq;
         finished();
