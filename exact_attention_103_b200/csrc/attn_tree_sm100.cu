@@ -38,8 +38,8 @@
 //
 // Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
 // 64 ragged contexts of 512 to 8192, one token, bf16: 144 (86%).  Two contexts of 131072, 64 rows,
-// E4M3: 133 (59%; the softmax with its conversions bounds it).  A call of little work costs
-// 11 to 13: two launches and about seven round trips to memory behind one another.
+// E4M3: 129 (61%; the softmax with its conversions bounds it).  A call of little work costs
+// 11 to 12: two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -89,6 +89,7 @@ struct TreeParams {
   int box_rows;    // rows of one K/V copy: min(page size, 128)
   int tpt;         // tokens of a 128-row tile: 128 / G
   int tpt32;       // tokens of a swapped item's copy of q: kSwapped / G
+  uint32_t inv_g;  // ceil(2^32 / G): rows up to 2^24 are divided by its high product; 0: G = 1
   float scale_log2, o_scale, tau, p_shift;
   float* part;     // [grid][2][D / 4][256][4] unnormalised O: four columns of neighbouring rows
                    // lie together, as the lanes that write and join them are neighbouring rows
@@ -147,6 +148,9 @@ struct Layout {
   }
 };
 
+__device__ __forceinline__ int token_of(int row, const TreeParams& p) {  // row / G
+  return p.inv_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.inv_g)) : row;
+}
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // One CTA's stretch of an item: key tiles [j0, j1) of kvt (none if j0 >= j1).
@@ -167,10 +171,13 @@ struct Seg {
 // behind the other: the cost of beginning it, then each key tile as long as its cost (`one` or
 // `pair` of row tiles).  A tile belongs to the CTA whose part holds its first unit; parts are no
 // shorter than the longest tile, so a part among an item's tiles holds one of them.  Tables in
-// shared memory, per sequence: cum (cost before it), first row of q, slot, tokens in the cache.
+// shared memory, per sequence: cum (cost before it), its cost per cache head, first row of q, slot,
+// tokens in the cache.  The decoding stands before every item's products, so it divides by constants or
+// by way of a reciprocal.
+template <int one, int pair, int item>
 struct List {
-  const int *cum, *cu, *slot, *len;
-  int B, heads, G, tpt, one, pair, item;
+  const int *cum, *per, *cu, *slot, *len;
+  int B, G, tpt;
   bool masked, split;
 
   // Key tiles of row pair rt of a sequence: without a mask its last token sees no further
@@ -192,9 +199,11 @@ struct List {
     s.slot = slot[lo];
     s.len = len[lo];
     s.ctx = s.len - s.n;
-    const int per_head = (cum[lo + 1] - cum[lo]) / heads;
+    const int per_head = per[lo];
     int r = x - cum[lo];
-    s.h = r / per_head;
+    s.h = static_cast<int>(__fdividef(static_cast<float>(r), static_cast<float>(per_head)));  // off by one at most
+    if (s.h * per_head > r) --s.h;
+    else if ((s.h + 1) * per_head <= r) ++s.h;
     r -= s.h * per_head;
     int rt = 0, kv = tiles(s.n, s.len, 0), w = cost(s.n, 0);
     while (r >= item + kv * w) {
@@ -213,8 +222,9 @@ struct List {
     s.kvt = kv;
     s.begin = x - r;
     s.next = min(end, s.begin + item + kv * w);
-    s.j0 = ceil_div(max(0, r - item), w);
-    s.j1 = ceil_div(max(0, s.next - s.begin - item), w);
+    const int a = max(0, r - item), b = max(0, s.next - s.begin - item);
+    s.j0 = s.two ? ceil_div(a, pair) : ceil_div(a, one);
+    s.j1 = s.two ? ceil_div(b, pair) : ceil_div(b, one);
     return s;
   }
 };
@@ -290,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::MISC_OFF);
   // misc[0] TMEM base, misc[1] abort flag, misc[2] items finished, misc[4..16) sums of the warps
   int* tab = reinterpret_cast<int*>(smem + Lay::TABLE_OFF);
-  int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B;
+  int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B, *t_per = t_len + p.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   let_next_launch();
@@ -338,18 +348,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       32 * (static_cast<int>(threadIdx.x) - b * lines)));
     }
   }
-  List list;
+  List<Lay::COST_ONE, Lay::COST_PAIR, Lay::COST_ITEM> list;
   list.cum = t_cum;
+  list.per = t_per;
   list.cu = t_cu;
   list.slot = t_slot;
   list.len = t_len;
   list.B = p.B;
-  list.heads = p.heads;
   list.G = p.G;
   list.tpt = p.tpt;
-  list.one = Lay::COST_ONE;
-  list.pair = Lay::COST_PAIR;
-  list.item = Lay::COST_ITEM;
   list.masked = p.mask != nullptr;
   list.split = F8;
   {
@@ -375,7 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bad) {
           record_invalid(p.err, bad);
         } else {
-          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += list.item + list.tiles(n, len, rt) * list.cost(n, rt);
+          for (int rt = 0; rt * 2 * p.tpt < n; ++rt) work += Lay::COST_ITEM + list.tiles(n, len, rt) * list.cost(n, rt);
+          t_per[b] = work;
           work *= p.heads;
         }
       }
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // E4M3(x - hi).  A row is held by D / 8 lanes, 8 values each; a warp's rows are 8 kRows apart.
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   auto load_q = [&](const Seg& it, int r) -> uint4 {
-    const int t = r / p.G;
+    const int t = token_of(r, p);
     const __nv_bfloat16* q = p.q + (static_cast<int64_t>(it.q0 + it.tok0) * p.Hq + it.h * p.G) * D + 8 * (lane % kLanes);
     if (r >= it.nt * p.G) return make_uint4(0, 0, 0, 0);
     return __ldcg(reinterpret_cast<const uint4*>(q + (static_cast<int64_t>(t) * (p.Hq - p.G) + r) * D));
@@ -822,26 +830,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++w_pv;
       }
       if (!behind()) return false;
-      // Row sums over the keys (lanes, then warps): a lane ends with row 32 b + lane.
+      // Row sums over the keys (lanes, then warps): each step adds a lane's other half of the rows, so
+      // that a lane ends with row lane % N.
+      {
+        float v[N];
 #pragma unroll
-      for (int b = 0; b < (N + 31) / 32; ++b) {
-        {
-          float v[32];
+        for (int i = 0; i < N; ++i) v[i] = l[i];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 32 * b + i < N ? l[32 * b + i < N ? 32 * b + i : 0] : 0.f;
+        for (int o = N / 2; o; o >>= 1) {
 #pragma unroll
-          for (int o = 16; o; o >>= 1) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (i < o) {
-                const bool up = (lane & o) != 0;
-                const float give = up ? v[i] : v[i + o], have = up ? v[i + o] : v[i];
-                v[i] = have + __shfl_xor_sync(0xffffffffu, give, o);
-              }
-            }
+          for (int i = 0; i < o; ++i) {
+            const bool up = (lane & o) != 0;
+            const float give = up ? v[i] : v[i + o], have = up ? v[i + o] : v[i];
+            v[i] = have + __shfl_xor_sync(0xffffffffu, give, o);
           }
-          wm[wq * 64 + 32 * b + lane] = v[0];
         }
+        if constexpr (N == 16) v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+        wm[wq * 64 + lane] = v[0];
       }
       if (first && key < 64) mr[key] = -INFINITY;  // no tile for this stream
       __syncwarp();
@@ -867,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nm[key] = w0 * f0;
         al[key] = w1 * f0;
         if (s == 0) {
-          const int t2 = key / p.G, g2 = key - t2 * p.G;
+          const int t2 = token_of(key, p), g2 = key - t2 * p.G;
           if (whole)
             p.lse[static_cast<int64_t>(it.h * p.G + g2) * p.T + it.q0 + it.tok0 + t2] =
                 sum > 0.f ? (m + __log2f(sum) - p.p_shift) * kLn2 : -INFINITY;
@@ -879,35 +884,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(Lay::B_OFULL, o_phase, kSiteTOFull)) return false;
       o_phase ^= 1u;
       tc_fence_after();
-      // O^T: lane = dimension; this warpgroup takes every other group of 8 rows.
+      // O^T: lane = dimension; this warpgroup takes every other group of 4 rows.
       if (wq * 32 < D) {
         const uint32_t t0 = tmem + lane_bits + Lay::TM_O0, t1 = tmem + lane_bits + Lay::TM_O1;
-        for (int c = s; 8 * c < rows; c += 2) {
-          float v[8];
-          uint32_t w[8];
+        for (int c = 4 * s; c < rows; c += 8) {
+          float v[4] = {0.f, 0.f, 0.f, 0.f};
+          auto add = [&](uint32_t at, const float* weight) {
+            uint32_t w[8];
+            tmem_ld_x8(at + c, w);  // of the 8 columns from there (there are that many) the first 4
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(__uint_as_float(w[i]), weight[c + i], v[i]);
+          };
 #pragma unroll
           for (int term = 0; term < (F8 ? 2 : 1); ++term) {
-            tmem_ld_x8(t0 + 8 * c + N * term, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), nm[8 * c + i], v[i]);
-            if (nj > 1) {
-              tmem_ld_x8(t1 + 8 * c + N * term, w);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = fmaf(__uint_as_float(w[i]), al[8 * c + i], v[i]);
-            }
+            add(t0 + N * term, nm);
+            if (nj > 1) add(t1 + N * term, al);
           }
+          int t2 = token_of(c, p), g2 = c - t2 * p.G;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = 8 * c + i;
+          for (int i = 0; i < 4; ++i) {
+            const int row = c + i;
             if (row < rows) {
-              const int t2 = row / p.G, g2 = row - t2 * p.G;
               if (whole)
                 p.o[(static_cast<int64_t>(it.q0 + it.tok0 + t2) * p.Hq + it.h * p.G + g2) * D + key] = __float2bfloat16(v[i]);
               else
                 p.part[((slot * (D / 4) + (key >> 2)) * (2 * kBM) + row) * 4 + (key & 3)] = v[i];
             }
+            if (++g2 == p.G) ++t2, g2 = 0;
           }
         }
       }
@@ -927,7 +930,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it.j0 >= it.j1) continue;
       if (threadIdx.x == 0 && it.j0 == 0 && it.j1 < it.kvt) {
         // The item's first tiles without its last: the CTA whose part holds the first unit of the item's last tile
-        const int64_t end = it.begin + list.item + (it.kvt - 1) * (it.two ? list.pair : list.one);
+        const int64_t end = it.begin + Lay::COST_ITEM + (it.kvt - 1) * (it.two ? Lay::COST_PAIR : Lay::COST_ONE);
         int last = static_cast<int>(end * ctas / total);
         while (static_cast<int64_t>(last + 1) * total / ctas <= end) ++last;
         while (static_cast<int64_t>(last) * total / ctas > end) --last;
@@ -937,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int mine = it.two ? (s ? it.nt - p.tpt : p.tpt) : it.nt;
       // The warp's rows of the tile, this thread's row of it, and that row's token.
       const int row_n = it.duo ? 16 : 32, row0 = wq * row_n, rr = row0 + (lane & (row_n - 1));
-      const int tl = rr / p.G;
+      const int tl = token_of(rr, p);
       const int tok = it.tok0 + first + tl;  // of the sequence
       const bool valid = tl < mine;
       const bool busy = row0 < mine * p.G;   // the warp has a valid row
@@ -954,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (p.mask != nullptr && it.j1 * kBN > it.ctx) {
         // The mask rows of this warp's tokens will be needed for the last tiles.
-        const int t0 = it.swapped ? 0 : row0 / p.G, t1 = it.swapped ? it.nt - 1 : min((row0 + row_n - 1) / p.G, mine - 1);
+        const int t0 = it.swapped ? 0 : token_of(row0, p), t1 = it.swapped ? it.nt - 1 : min(token_of(row0 + row_n - 1, p), mine - 1);
         const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first + t0) * p.mask_width;
         for (int i = lane * 128; i < (t1 - t0 + 1) * p.mask_width; i += 32 * 128)
           asm volatile("prefetch.global.L1 [%0];" ::"l"(rows + i));
@@ -1044,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 2; ++c) vis[c] = below(it.ctx - kb, c);
               // The mask rows of the warp's tokens, 32 columns per load, 8 tokens at a time.
-              const int t_lo = row0 / p.G, t_hi = min((row0 + row_n - 1) / p.G, mine - 1);
+              const int t_lo = token_of(row0, p), t_hi = min(token_of(row0 + row_n - 1, p), mine - 1);
               const uint8_t* rows = p.mask + static_cast<int64_t>(it.q0 + it.tok0 + first) * p.mask_width;
               const int col = kb + lane - it.ctx;
               for (int t0 = t_lo; t0 <= t_hi; t0 += 8) {
@@ -1549,7 +1552,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int i = blockIdx.y * 128 + threadIdx.x;
   const int col = i / rows, j = i - col * rows;  // columns 4 col.., row j: token j / G, head j % G
   if (col >= D / 4) return;
-  const int t = j / p.G, g = j - t * p.G;
+  const int t = token_of(j, p), g = j - t * p.G;
   const int tile = t / p.tpt;
   const int r = tile * kBM + (t - tile * p.tpt) * p.G + g;
   const int parts = hd.w - c + 1;
@@ -1604,8 +1607,8 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tq32, const CUten
                      int rows, cudaStream_t st) {
   using Lay = Layout<D, F8>;
   auto kern = tree_kernel<D, F8>;
-  const int smem = 1024 + Lay::TABLE_OFF + (4 * p.B + 2) * 4;
-  static_assert(1024 + Lay::TABLE_OFF + (4 * 1024 + 2) * 4 <= kMaxSmem, "tables of 1024 sequences fit");
+  const int smem = 1024 + Lay::TABLE_OFF + (5 * p.B + 2) * 4;
+  static_assert(1024 + Lay::TABLE_OFF + (5 * 1024 + 2) * 4 <= kMaxSmem, "tables of 1024 sequences fit");
   // Once per device: the call costs the host more than a tensor map does.
   static std::atomic<uint64_t> ready{0};
   int dev = 0;
@@ -1654,6 +1657,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   p.rows = c.layers * c.pages * c.page_size;
   p.box_rows = c.page_size < kBN ? c.page_size : kBN;
   p.tpt = kBM / p.G;
+  p.inv_g = p.G > 1 ? 0xffffffffu / p.G + 1 : 0u;
   p.tpt32 = kSwapped / p.G;
   const bool f8 = c.e4m3 != 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
