@@ -37,8 +37,8 @@
 // copies and products, frees TMEM and returns.
 //
 // Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
-// 64 ragged contexts of 512 to 8192, one token, bf16: 144 (86%).  Two contexts of 131072, 64 rows,
-// E4M3: 129 (61%; the softmax with its conversions bounds it).  A call of little work costs
+// 64 ragged contexts of 512 to 8192, one token, bf16: 145 (86%).  Two contexts of 131072, 64 rows,
+// E4M3: 128 (62%; the softmax with its conversions bounds it).  A call of little work costs
 // 11 to 12: two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
