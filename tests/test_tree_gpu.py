@@ -361,6 +361,57 @@ def test_repeatable_on_streams_and_in_graphs():
     ea.get_device_status()
 
 
+@pytest.mark.parametrize("dtype", list(SCALES))
+def test_one_slot_for_two_sequences_layers_and_scales(dtype):
+    """Reading is shared freely: two sequences of a call may be the same slot, in any layer, with any
+    scale; a strided cache of several layers is read in place."""
+    c = build([300, 40], [5, 5], 2, 128, 32, dtype, seed=21, layers=3)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randn((15, 8, 128), generator=g, device="cuda").to(torch.bfloat16)
+    q[5:10] = q[:5]
+    cu = ints([0, 5, 10, 15])
+    # scales below 1 / sqrt(d), which the tolerances assume; the two sequences need not be bitwise
+    # alike, as their keys may be split over the SMs at different places
+    for layer, scale in ((2, 0.05), (0, 0.02)):
+        o, lse = ea.tree_fwd(c, q, cu, slots=ints([0, 0, 1]), layer=layer, scale=scale)
+        ea.get_device_status()
+        verify(c, q, cu, None, o, lse, slots=[0, 0, 1], layer=layer, scale=scale)
+
+
+def test_append_in_place_and_page_calls_on_another_stream():
+    heads, d, page = 2, 128, 16
+    plan = ea.Rope(d)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = (torch.randn((9, h, d), generator=g, device="cuda").to(torch.bfloat16) for h in (8, heads, heads))
+    cu, slots, want = ints([0, 4, 9]), ints([1, 2]), ints([20, 33])
+    caches, outs = [], []
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        c = ea.KVCache.empty(1, 20, page, heads, d, 4, 8)
+        c.k.zero_(), c.v.zero_()
+        torch.cuda.synchronize()
+        x = q.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        assert c.alloc(slots, want, stream=stream) is not None
+        y = ea.rope_append(c, x, k, v, cu, plan=plan, slots=slots, out=x, stream=stream)
+        assert y is x
+        c.fork(ints([1]), ints([3]), stream=stream)
+        o, lse = ea.tree_fwd(c, x, cu, slots=slots, stream=stream)
+        c.compact(cu, ints([[0, 3], [4, -1]]), ints([2, 1]), slots=slots, stream=stream)
+        c.free(ints([3]), stream=stream)
+        torch.cuda.synchronize()
+        ea.get_device_status()
+        caches.append(c)
+        outs.append((x, o, lse))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    for name in ("k", "v", "page_table", "lens", "refs"):
+        assert torch.equal(getattr(caches[0], name), getattr(caches[1], name))
+    turned = ea.rope_fwd(plan, q, positions=torch.cat([torch.arange(16, 20), torch.arange(28, 33)]).to(torch.int32).cuda(),
+                         cu_seqlens=cu)
+    assert torch.equal(outs[0][0], turned)
+
+
 def test_a_step_in_a_graph():
     """Pages, append, attention and compaction of a decoding step, captured once and replayed on
     another stream: every replay continues from the state that the last one left."""
