@@ -135,10 +135,10 @@ struct Layout {
   static constexpr int TABLE_OFF = MISC_OFF + 128;
   // Cost of a key tile with one and with two row tiles, and of beginning an item (its mask, queries
   // and epilogue), in units of about 1000 to 1300 cycles, as homogeneous batches and then mixed ones
-  // measured: 16 trees of 48 tokens, bf16, 121 us with 2, 3, 7 and 114 with 4, 7, 24; 64 single tokens,
-  // E4M3, 124 with an item at 12 and 113 at 24.
+  // measured.  With an item at 12, 20, 28 (bf16 d 128, us): 256 single tokens over 50 to 2000 167, 157,
+  // 161; 16 trees of 48 tokens 118, 113, 113; 128 single tokens over 100 to 4000 112, 115, 120.
   static constexpr int COST_ONE = !F8 && D == 128 ? 4 : 2, COST_PAIR = !F8 && D == 128 ? 7 : 4,
-                       COST_ITEM = F8 || D == 128 ? 24 : 12;
+                       COST_ITEM = F8 || D == 128 ? 20 : 10;
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -1678,7 +1678,7 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   // describe.
   const int64_t items = (static_cast<int64_t>(a.B) + a.T / (2 * p.tpt)) * c.heads;
   const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + kBN - 1) / kBN;
-  if (items > INT32_MAX / (7 * tiles + 24)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 7, an item 24
+  if (items > INT32_MAX / (7 * tiles + 20)) return ATTN_ERR_UNSUPPORTED;  // a tile costs at most 7, an item 20
   int grid = static_cast<int>(items * tiles < sms ? items * tiles : sms);
   if (grid > kMaxGrid) grid = kMaxGrid;
   const int rows = (a.T < 2 * p.tpt ? a.T : 2 * p.tpt) * p.G;

@@ -9,7 +9,7 @@ import re
 import pytest
 
 SOURCE = (pathlib.Path(__file__).parents[1] / "exact_attention_103_b200" / "csrc" / "attn_tree_sm100.cu").read_text()
-COSTS = [(4, 7, 24), (2, 4, 12), (2, 4, 24)]  # one row tile, two, beginning an item: bf16 d 128, bf16 d 64, E4M3
+COSTS = [(4, 7, 20), (2, 4, 10), (2, 4, 20)]  # one row tile, two, beginning an item: bf16 d 128, bf16 d 64, E4M3
 MIN_PART = int(re.search(r"constexpr int kMinPart = (\d+);", SOURCE).group(1))
 
 
