@@ -25,11 +25,14 @@
 //    computed transposed, a key per thread (swapped items).
 //
 // E4M3 caches: the keys and values go to the tensor cores as they are (kind::f8f6f4), and the
-// other operand of each product is split into two E4M3 terms, hi + lo, which keeps bf16's
-// precision: a bf16 query scaled by a power of two (its row's largest value in [128, 256)) is
-// hi + lo to 2^-9 of that scale, and hi + lo holds P~ to 2^-8 (the first term keeps 4
-// significant bits, the second 4 more).  Each costs one more product, at twice bf16's rate; up to
-// 64 rows both terms are rows of one product (duo items), or columns of it (swapped items).
+// other operand of each product is a sum of 8-bit terms that keeps bf16's precision.  A bf16 query
+// scaled by a power of two (its row's largest value in [128, 256)) is hi + lo, two E4M3 terms, to
+// 2^-17 of the row's largest value.  P~ needs E4M3's precision over far more than its range, as many small
+// weights beside a large one may hold most of a row: it is rounded to fp16 and split into three E5M2
+// terms (3 bits each), off by 2^-9 of itself or 2^-28 of the row's reference.  (Two E4M3 terms lost
+// every weight below 2^-14 of the reference: with one key 11 nats above 4096 others, 40% of O.)  A term
+// costs one more product, at twice bf16's rate; up to 64 rows the first two are rows of one product (duo
+// items) and up to 32 all of them are columns of one (swapped items).
 //
 // Warp roles (384 threads): 0-3 and 4-7 softmax, correction and epilogue of streams 0 and 1;
 // 8 and 10 TMA producers of K (and q) and of V; 9 (TMEM owner) and 11 issue S and P~V.  The softmax
@@ -139,6 +142,7 @@ struct Layout {
   // 161; 16 trees of 48 tokens 118, 113, 113; 128 single tokens over 100 to 4000 112, 115, 120.
   static constexpr int COST_ONE = !F8 && D == 128 ? 4 : 2, COST_PAIR = !F8 && D == 128 ? 7 : 4,
                        COST_ITEM = F8 || D == 128 ? 20 : 10;
+  static constexpr int P_TERMS = F8 ? 3 : 1;  // products that P~V is the sum of
   static constexpr int TM_S = 0, TM_O0 = 256, TM_O1 = 384;  // S: four buffers of 64 columns
   // Row `key` of stream s's P~ (a swapped item's), from the shared-memory base.
   __host__ __device__ static constexpr int p_row(int s, int key) {
@@ -162,8 +166,9 @@ struct Seg {
   int begin, next;        // where the item begins in the list, and the next stretch
   bool two;               // more than one row tile
   bool swapped;           // at most kSwapped rows, all of the sequence's
-  // E4M3, at most kDuo rows: the two terms of a split operand are rows of one product, hi of row i
-  // in lane 32 (i / 16) + i % 16, lo 16 lanes behind; two threads of the warp share the row.
+  // E4M3, at most kDuo rows: two terms of a split operand are rows of one product, hi of row i
+  // in lane 32 (i / 16) + i % 16, lo 16 lanes behind; two threads of the warp share the row.  The third
+  // term of P~ is a product of its own, with zeros in the lo rows.
   bool duo;
 };
 
@@ -256,6 +261,7 @@ __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, uint64
   return true;
 }
 
+constexpr uint32_t kE5m2A = 1u << 7, kE5m2B = 1u << 10;  // instruction descriptor: that operand is E5M2, not E4M3
 constexpr uint32_t kLoLanes = 16u << 16;  // from the hi rows of a duo item to its lo rows, as a TMEM address
 
 // Rows of a swapped item's products.
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < NCH; ++c) {
 #pragma unroll
-              for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+              for (int term = 0; term < Lay::P_TERMS; ++term) {
                 uint32_t w[16];
                 const uint32_t at = t_o + N * term + 16 * c;
                 tmem_ld_x16(at, w);
@@ -801,19 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // 16-byte units of a key's row, permuted as the descriptors' 128-byte swizzle
             if constexpr (F8) {
-              uint32_t hi[4], lo[4];
+              uint32_t t[3][4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float h4[4], l4[4];
-                upper4_x2(h4[0], h4[1], e[4 * i], e[4 * i + 1]);
-                upper4_x2(h4[2], h4[3], e[4 * i + 2], e[4 * i + 3]);
-                fsub2(l4[0], l4[1], e[4 * i], e[4 * i + 1], h4[0], h4[1]);
-                fsub2(l4[2], l4[3], e[4 * i + 2], e[4 * i + 3], h4[2], h4[3]);
-                hi[i] = pack_e4m3x2(h4[0], h4[1]) | (pack_e4m3x2(h4[2], h4[3]) << 16);
-                lo[i] = pack_e4m3x2(l4[0], l4[1]) | (pack_e4m3x2(l4[2], l4[3]) << 16);
-              }
-              *reinterpret_cast<uint4*>(prow + ((c ^ (key & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-              *reinterpret_cast<uint4*>(prow + (((NCH + c) ^ (key & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              for (int i = 0; i < 4; ++i)
+                split_e5m2x4(e[4 * i], e[4 * i + 1], e[4 * i + 2], e[4 * i + 3], t[0][i], t[1][i], t[2][i]);
+#pragma unroll
+              for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint4*>(prow + (((NCH * k + c) ^ (key & 7)) << 4)) = make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
             } else {
 #pragma unroll
               for (int k = 0; k < 2; ++k)
@@ -896,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) v[i] = fmaf(__uint_as_float(w[i]), weight[c + i], v[i]);
           };
 #pragma unroll
-          for (int term = 0; term < (F8 ? 2 : 1); ++term) {
+          for (int term = 0; term < Lay::P_TERMS; ++term) {
             add(t0 + N * term, nm);
             if (nj > 1) add(t1 + N * term, al);
           }
@@ -1119,30 +1119,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tmem_st_x32(t_s, pk);
           } else {
-            // P~ = hi + lo; the conversion of hi is exact while it is a normal E4M3 number.
-            uint32_t hi[NC / 4], lo[NC / 4];
+            uint32_t t1[NC / 4], t2[NC / 4], t3[NC / 4];
 #pragma unroll
-            for (int c = 0; c < NC / 2; ++c) {
-              float a, e;
-              exps(c, a, e);
-              float ha, he, la, le;
-              upper4_x2(ha, he, a, e);
-              fsub2(la, le, a, e, ha, he);
-              const uint32_t wh = pack_e4m3x2(ha, he), wl = pack_e4m3x2(la, le);
-              if (c & 1) {
-                hi[c >> 1] |= wh << 16;
-                lo[c >> 1] |= wl << 16;
-              } else {
-                hi[c >> 1] = wh;
-                lo[c >> 1] = wl;
-              }
+            for (int c = 0; c < NC / 4; ++c) {
+              float e[4];
+              exps(2 * c, e[0], e[1]);
+              exps(2 * c + 1, e[2], e[3]);
+              split_e5m2x4(e[0], e[1], e[2], e[3], t1[c], t2[c], t3[c]);
             }
             if constexpr (W == 1) {
-              tmem_st_x16(t_s, hi);
-              tmem_st_x16(t_s + 16, lo);
+              tmem_st_x16(t_s, t1);
+              tmem_st_x16(t_s + 16, t2);
+              tmem_st_x16(t_s + 32, t3);
             } else {
-              tmem_st_duo(t_s, hi);
-              tmem_st_duo(t_s + kLoLanes, lo);
+              const uint32_t none[NC / 4] = {};
+              tmem_st_duo(t_s, t1);
+              tmem_st_duo(t_s + kLoLanes, t2);
+              tmem_st_duo(t_s + 16, t3);
+              tmem_st_duo(t_s + 16 + kLoLanes, none);
             }
           }
           if (again && __any_sync(0xffffffffu, need)) {
@@ -1310,8 +1304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++items;
         if (it.swapped) {
           // S^T = K Q^T (128 keys x N rows) and O^T += V^T P~^T (d x N), N the item's rows rounded up.
-          // Split operands: S sums both terms; O has 2 N columns, hi's and lo's.  d = 64: V's 64 rows
-          // twice (LBO 0).
+          // Split operands: S sums both terms of q; O has 3 N columns, N for each term of P~.  d = 64: V's 64
+          // rows twice (LBO 0).
           const uint32_t N = static_cast<uint32_t>(swapped_rows(it.nt * p.G));
           if (warp == 9) {
             const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 0, 0) : idesc_bf16_f32(kBM, 0, 0, 0)) | ((N >> 3) << 17);
@@ -1351,7 +1345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               __syncwarp();
             }
           } else {
-            const uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, 0, 1, 1) | ((N >> 2) << 17) : idesc_bf16_f32(kBM, 0, 1, 1) | ((N >> 3) << 17);
+            const uint32_t idesc = (F8 ? idesc_e4m3_f32(kBM, 0, 1, 1) | kE5m2B : idesc_bf16_f32(kBM, 0, 1, 1)) | ((Lay::P_TERMS * N >> 3) << 17);
             constexpr int NK = kBN / Lay::KSTEP;
             constexpr int LBO = D == 64 ? 0 : Lay::CHUNK;
             for (int j = 0; j < nj && ok; ++j) {
@@ -1466,7 +1460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
         } else {
-          constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) : idesc_bf16_f32(kBM, D, 0, 1);
+          constexpr uint32_t idesc = F8 ? idesc_e4m3_f32(kBM, D, 0, 1) | kE5m2A : idesc_bf16_f32(kBM, D, 0, 1);
           constexpr int NK = kHalf / Lay::KSTEP;
           for (int v = 0; v < rounds && ok; ++v) {
             for (int s = 0; s < 2; ++s) {
@@ -1496,8 +1490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                   const uint64_t dv = desc_add(dv0, kk * Lay::KSTEP * Lay::ROWB);
                   const uint32_t acc = kk > 0 ? 1u : more;
                   if constexpr (F8) {
-                    mma_ts_f8(tO, tP + kk * 8, dv, idesc, acc);
-                    if constexpr (decltype(terms)::value == 2) mma_ts_f8(tO, tP + 16 + kk * 8, dv, idesc, 1u);
+#pragma unroll
+                    for (int term = 0; term < decltype(terms)::value; ++term)
+                      mma_ts_f8(tO, tP + 16 * term + kk * 8, dv, idesc, term > 0 ? 1u : acc);
                   } else {
                     mma_ts(tO, tP + kk * 8, dv, idesc, acc);
                   }
@@ -1505,11 +1500,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (F8 && it.duo) {
 #pragma unroll
                   for (int kk = 0; kk < NK; ++kk)
-                    if (kk < steps) product(kk, std::integral_constant<int, 1>{});
+                    if (kk < steps) product(kk, std::integral_constant<int, 2>{});
                 } else {
 #pragma unroll
                   for (int kk = 0; kk < NK; ++kk)
-                    if (kk < steps) product(kk, std::integral_constant<int, 2>{});
+                    if (kk < steps) product(kk, std::integral_constant<int, 3>{});
                 }
                 tc_commit(bar(Lay::B_PVDONE + buf));
                 if (tile_ends) tc_commit(bar(Lay::B_KVEMPTY + slot));
@@ -1662,11 +1657,11 @@ attn_status_t launch_tree(const TreeArgs& a, int sms, cudaStream_t st, cudaError
   const bool f8 = c.e4m3 != 0;
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (f8 ? static_cast<double>(c.k_scale) : 1.0));
   p.o_scale = f8 ? c.v_scale : 1.f;
-  // P~ <= 2^tau; on the E4M3 path it carries 2^p_shift, so that at most 256 of E4M3's 448 is
-  // reached.  tau 4 rather than 2: a maximum of 64 rows grew by 2 in most tiles (a rescale
-  // each), by 4 in few; small weights still keep 2^-9 absolute of the row's reference 2^4.
+  // P~ <= 2^tau; on the E4M3 path it carries 2^p_shift, so that at most 2^15 of fp16's 65504 and E5M2's
+  // 57344 is reached, and the terms' smallest half step, 2^-17, is 2^-28 of the row's reference.  tau 4
+  // rather than 2: a maximum of 64 rows grew by 2 in most tiles (a rescale each), by 4 in few.
   p.tau = f8 ? 4.f : 8.f;
-  p.p_shift = f8 ? 4.f : 0.f;
+  p.p_shift = f8 ? 11.f : 0.f;
   p.err = a.err;
   char* ws = static_cast<char*>(a.ws);
   p.part = reinterpret_cast<float*>(ws);

@@ -46,6 +46,32 @@ __device__ __forceinline__ void upper4_x2(float& h0, float& h1, float x0, float 
   fsub2(h0, h1, t0, t1, u0, u1);
 }
 
+// Four non-negative values below 2^16 as three E5M2 terms each, one byte per value and term.  E5M2 is
+// the upper byte of fp16: each value is rounded to fp16 (2^-11), the first two terms are upper bytes cut
+// off, what they leave is exact in fp16, and the last is rounded.  The first leaves less than 2^-2 of the
+// value's power of two, the second less than 2^-5, the third at most 2^-9, or half of E5M2's smallest
+// step, 2^-17.  A NaN stays one in the first term.
+__device__ __forceinline__ uint32_t fp16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t less_upper_bytes(uint32_t x) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(x & 0xff00ff00u));
+  return r;
+}
+__device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float x3, uint32_t& t1, uint32_t& t2, uint32_t& t3) {
+  const uint32_t a = fp16_pair(x0, x1), b = fp16_pair(x2, x3);
+  const uint32_t ar = less_upper_bytes(a), br = less_upper_bytes(b);
+  // half of the last term's step, carried into its upper byte; halves of fp16 numbers never
+  // overflow into one another, as what is left is small
+  const uint32_t as = less_upper_bytes(ar) + 0x00800080u, bs = less_upper_bytes(br) + 0x00800080u;
+  t1 = __byte_perm(a, b, 0x7531);
+  t2 = __byte_perm(ar, br, 0x7531);
+  t3 = __byte_perm(as, bs, 0x7531);
+}
+
 // 16 columns of this warp's 32 lanes, complete on return (as tmem_ld_x8 and its wider forms).
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
