@@ -261,10 +261,10 @@ __device__ __forceinline__ void drop(const attn_cache_t& c, int page, int* err) 
   }
 }
 
-// Takes a reference from entries [m0, m1) of a slot's table row and clears them.
-__device__ __forceinline__ void release(const attn_cache_t& c, int slot, int m0, int m1, int* err) {
+// Takes a reference from entries [m0, m1) of a slot's table row and clears them: thread t of n.
+__device__ __forceinline__ void release(const attn_cache_t& c, int slot, int m0, int m1, int t, int n, int* err) {
   int32_t* row = c.page_table + static_cast<int64_t>(slot) * c.max_pages;
-  for (int m = m0 + threadIdx.x; m < m1; m += blockDim.x) {
+  for (int m = m0 + t; m < m1; m += n) {
     const int p = __ldcg(row + m);
     row[m] = -1;
     drop(c, p, err);
@@ -292,7 +292,7 @@ __global__ void free_kernel(const attn_cache_t c, const int32_t* slots, int* err
     row[m] = -1;
     drop(c, p, err);
   }
-  release(c, slot, blockDim.x, count, err);
+  release(c, slot, blockDim.x, count, threadIdx.x, blockDim.x, err);
 }
 
 __global__ void copy_kernel(const attn_cache_t c, const int32_t* src, const int32_t* dst, int n, int chunks, int* err) {
@@ -324,44 +324,37 @@ __global__ void copy_kernel(const attn_cache_t c, const int32_t* src, const int3
   }
 }
 
-// What compact does with sequence b; decided the same way by both of its kernels.
+// What compact does with sequence b.  Both of its kernels decide it, from the same lengths, tables and
+// reference counts: neither changes any of them before every sequence has been decided.
 struct Kept {
   int slot, base, len, count;
-  bool ok;
 };
-__device__ __forceinline__ Kept kept_of(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
-                                        const int32_t* accepted, const int32_t* slots, int b, int* err) {  // err null: another kernel says it
-  Kept k;
+// The share of thread t of n in the checks of sequence b: 0, or the site of what is wrong.
+__device__ __forceinline__ int check_kept(const attn_cache_t& c, const int32_t* cu_q, const int32_t* path, int width,
+                                          const int32_t* accepted, const int32_t* slots, int b, int t, int n, Kept& k) {
   k.slot = slots ? __ldcg(slots + b) : b;
+  k.len = k.base = k.count = 0;
+  if (k.slot < 0 || k.slot >= c.slots) return kSiteSlot;
+  const int drafted = __ldcg(cu_q + b + 1) - __ldcg(cu_q + b);
+  k.len = __ldcg(c.lens + k.slot);
+  k.count = __ldcg(accepted + b);
+  k.base = k.len - drafted;
   int bad = 0;
-  if (k.slot < 0 || k.slot >= c.slots) {
-    bad = kSiteSlot;
-    k.len = k.base = k.count = 0;
-  } else {
-    const int n = __ldcg(cu_q + b + 1) - __ldcg(cu_q + b);
-    k.len = __ldcg(c.lens + k.slot);
-    k.count = __ldcg(accepted + b);
-    k.base = k.len - n;
-    if (n < 0 || k.base < 0 || k.len > static_cast<int64_t>(c.max_pages) * c.page_size) bad = kSiteLength;
-    else if (k.count < 0 || k.count > n || k.count > width) bad = kSitePath;
-    if (!bad) {
-      const int32_t* row = path + static_cast<int64_t>(b) * width;
-      for (int i = threadIdx.x; i < k.count; i += blockDim.x) {
-        const int p = row[i];  // by way of L1: read again for the moves
-        if (p >= n || p <= (i ? row[i - 1] : -1)) {
-          bad = kSitePath;
-        } else if (p != i) {  // a token moves here: no other slot may hold the page
-          const int page = __ldcg(c.page_table + static_cast<int64_t>(k.slot) * c.max_pages + (k.base + i) / c.page_size);
-          if (page < 0 || page >= c.pages || __ldcg(c.refs + page) != 1) bad = kSitePage;
-        }
-      }
+  if (drafted < 0 || k.base < 0 || k.len > static_cast<int64_t>(c.max_pages) * c.page_size) return kSiteLength;
+  if (k.count < 0 || k.count > drafted || k.count > width) return kSitePath;
+  const int32_t* row = path + static_cast<int64_t>(b) * width;
+  for (int i = t; i < k.count; i += n) {
+    const int p = row[i];  // by way of L1: read again for the moves
+    if (p >= drafted || p <= (i ? row[i - 1] : -1)) {
+      bad = kSitePath;
+    } else if (p != i) {  // a token moves here: no other slot may hold the page
+      const int page = __ldcg(c.page_table + static_cast<int64_t>(k.slot) * c.max_pages + (k.base + i) / c.page_size);
+      if (page < 0 || page >= c.pages || __ldcg(c.refs + page) != 1) bad = kSitePage;
     }
-    for (int j = threadIdx.x; slots && j < b; j += blockDim.x)
-      if (__ldcg(slots + j) == k.slot) bad = kSiteSlot;
   }
-  if (bad && err) record_invalid(err, bad);
-  k.ok = !__syncthreads_or(bad);
-  return k;
+  for (int j = t; slots && j < b; j += n)
+    if (__ldcg(slots + j) == k.slot) bad = kSiteSlot;
+  return bad;
 }
 
 constexpr int kMoves = 128;  // moves whose rows are looked up together
@@ -377,8 +370,9 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
   let_next_launch();
   wait_for_previous();
   const int b = blockIdx.x;
-  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, b, nullptr);  // cut_kernel reports
-  if (!k.ok) return;
+  Kept k;
+  const int bad = check_kept(c, cu_q, path, width, accepted, slots, b, threadIdx.x, blockDim.x, k);  // cut_kernel reports it
+  if (__syncthreads_or(bad)) return;
   const int l = blockIdx.y >> 1, kv = blockIdx.y & 1;
   const int64_t rb = row_bytes(c);
   const int64_t col = (static_cast<int64_t>(blockIdx.z) * blockDim.x + threadIdx.x) * 16;
@@ -409,15 +403,33 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
   }
 }
 
-__global__ void cut_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
-                           const int32_t* accepted, const int32_t* slots, int* err) {
+// A warp per sequence, in one cluster of blocks: releasing pages changes the reference counts that other
+// sequences' checks read (two slots that share a page may be in one call), so the first page is
+// released when all sequences have been decided.
+constexpr int kCutWarps = 32, kCutBlocks = 8, kCutEach = kMaxSequences / (kCutWarps * kCutBlocks);
+__global__ void __launch_bounds__(kCutWarps * 32) cut_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path,
+                                                            int width, const int32_t* accepted, const int32_t* slots, int B,
+                                                            int* err) {
+  __shared__ Kept kept[kCutWarps][kCutEach];
   let_next_launch();
   wait_for_previous();  // the moves have read the table
-  const Kept k = kept_of(c, cu_q, path, width, accepted, slots, blockIdx.x, err);
-  if (!k.ok) return;
-  __syncthreads();  // every thread has read the length
-  if (threadIdx.x == 0) c.lens[k.slot] = k.base + k.count;
-  release(c, k.slot, pages_of(k.base + k.count, c.page_size), pages_of(k.len, c.page_size), err);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int n = 0;
+  for (int b = blockIdx.x * kCutWarps + warp; b < B; b += gridDim.x * kCutWarps, ++n) {
+    Kept k;
+    const int bad = check_kept(c, cu_q, path, width, accepted, slots, b, lane, 32, k);
+    if (bad) record_invalid(err, bad);
+    if (__any_sync(0xffffffffu, bad)) k.slot = -1;
+    if (lane == 0) kept[warp][n] = k;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  for (int i = 0; i < n; ++i) {
+    const Kept k = kept[warp][i];
+    if (k.slot < 0) continue;
+    if (lane == 0) c.lens[k.slot] = k.base + k.count;
+    release(c, k.slot, pages_of(k.base + k.count, c.page_size), pages_of(k.len, c.page_size), lane, 32, err);
+  }
 }
 
 }  // namespace
@@ -470,7 +482,9 @@ cudaError_t launch_compact(const attn_cache_t& c, const int32_t* cu_q, const int
   const int z = static_cast<int>((words + threads - 1) / threads);
   const cudaError_t e = launch_after(compact_kernel, dim3(B, 2 * c.layers, z), threads, 0, st, c, cu_q, path, width, accepted, slots, err);
   if (e != cudaSuccess) return e;
-  return launch_after(cut_kernel, B, 128, 0, st, c, cu_q, path, width, accepted, slots, err);
+  int blocks = 1;  // of the cluster: a power of two
+  while (blocks < kCutBlocks && blocks * kCutWarps < B) blocks *= 2;
+  return launch_clusters_after(cut_kernel, blocks, blocks, kCutWarps * 32, 0, st, c, cu_q, path, width, accepted, slots, B, err);
 }
 
 }  // namespace attn
