@@ -343,7 +343,9 @@ class KVCache:
               stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
         """Grows slot ``slots[i]`` to ``new_lens[i]`` tokens.  Pages are handed out in order
         of i, lowest number first; returns int32 ``granted[i]``: 1 iff request i needs no page
-        or requests 0..i need no more than are free.  One not granted changes nothing."""
+        or requests 0..i need no more than are free.  One not granted changes nothing.  A slot that
+        grows inside a page which another slot holds too (``compact`` may leave one) gets a page of its
+        own in its place, its tokens copied."""
         lib, dev, n = _lib_of(), self.device, slots.numel()
         granted = torch.empty(n, dtype=torch.int32, device=dev)
         _on(dev, lib.attn_cache_alloc, self._ref, _list(slots, "slots", dev),

@@ -48,6 +48,15 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
   return before + incl - v;
 }
 
+__device__ __forceinline__ int64_t row_bytes(const attn_cache_t& c) {
+  return static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2);
+}
+// K (kv = 0) or V of layer l, row `row` of its pages.
+__device__ __forceinline__ uint8_t* cache_row(const attn_cache_t& c, int l, int kv, int64_t row) {
+  return static_cast<uint8_t*>(kv ? c.v : c.k) +
+         (static_cast<int64_t>(l) * c.pages * c.page_size + row) * row_bytes(c);
+}
+
 // One fork, decided by the first kernel and carried out by the second.
 struct alignas(16) ForkItem {
   int src, dst, len;  // len 0: nothing to do
@@ -56,8 +65,10 @@ struct alignas(16) ForkItem {
 
 // Grants requests for pages.  alloc: slot a[i] grows to b[i] tokens.  FORK: slot a[i]
 // is forked into slot b[i] (the pages of its full part and the copies follow in
-// fork_kernel).  Shared memory: owner (first request that names a slot), upto (pages
-// needed by requests 0..i), have, slot.  One block, bound by its round trips to memory: the requests
+// fork_kernel).  A slot that grows inside a page which another slot holds too (compaction cut it back
+// there) gets a page of its own in its place, one page more, whose tokens this block copies itself: a launch
+// for it would cost every other call.  Shared memory: owner (first request that names a slot), upto (pages
+// needed by requests 0..i), have, slot, shared_page.  One block, bound by its round trips to memory: the requests
 // and the first 16384 reference counts, the lengths, the stores.  Measured (B200, in a graph): freeing
 // and granting 128 slots of a pool of 65536 pages 8.9 us, a grant that finds nothing to do 2.9 us.
 template <bool FORK>
@@ -69,6 +80,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
   int* upto = owner + c.slots;  // [n]
   int* have = upto + n;         // [n] pages held before (-1: refused)
   int* slot = have + n;         // [n] the slot that is written
+  int* shared_page = slot + n;  // [n] alloc: the page whose tokens are copied (-1: none)
   const int tid = threadIdx.x;
   const int32_t* target = FORK ? b : a;  // the slot that is written
   let_next_launch();
@@ -106,6 +118,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
     const int s = slot[i];
     bool ok = s >= 0 && s < c.slots && owner[s] == i;
     int site = kSiteSlot, need = 0, held = 0;
+    [[maybe_unused]] int alone = -1;
     if (FORK) {
       const int from = __ldcg(a + i);
       ok = ok && from >= 0 && from < c.slots && from != s;
@@ -125,10 +138,23 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
       if (ok) {
         held = pages_of(len, c.page_size);
         need = pages_of(want, c.page_size) - held;
+        if (want > len && (len & (c.page_size - 1))) {
+          const int last = __ldcg(c.page_table + static_cast<int64_t>(s) * c.max_pages + held - 1);
+          if (last < 0 || last >= c.pages) {
+            ok = false;
+            site = kSitePage;
+            need = 0;
+          } else if (__ldcg(c.refs + last) > 1) {
+            alone = last;
+            --held;
+            ++need;
+          }
+        }
       }
     }
     if (!ok) record_invalid(err, site);
     have[i] = ok ? held : -1;
+    if (!FORK) shared_page[i] = alone;
     sum += need;
     upto[i] = sum;  // within the thread; the threads before are added below
   }
@@ -168,6 +194,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
     bits = next;
   }
   __syncthreads();
+  bool copies = false;
   for (int i = i0; i < i1; ++i) {
     const int first = i ? upto[i - 1] : 0, need = upto[i] - first;
     bool ok = have[i] >= 0;
@@ -180,6 +207,10 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
         c.refs[__ldcg(e)] = 0;
         *e = -1;
       }
+      if (!FORK && shared_page[i] >= 0) {
+        c.page_table[static_cast<int64_t>(s) * c.max_pages + have[i]] = shared_page[i];
+        shared_page[i] = -1;
+      }
     }
     granted[i] = ok;
     if (FORK) {
@@ -188,7 +219,25 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
       if (!ok) items[i].len = 0;
       else c.lens[s] = items[i].len;
     } else if (ok) {
+      if (shared_page[i] >= 0) {
+        copies = true;
+        atomicSub(c.refs + shared_page[i], 1);
+        have[i] = __ldcg(c.page_table + static_cast<int64_t>(s) * c.max_pages + have[i]);  // the new page
+        slot[i] = __ldcg(c.lens + s) & (c.page_size - 1);                                 // its tokens
+      }
       c.lens[s] = __ldcg(b + i);
+    }
+  }
+  if (FORK || !__syncthreads_or(copies)) return;
+  for (int i = 0; i < n; ++i) {
+    if (shared_page[i] < 0) continue;
+    const int64_t from = static_cast<int64_t>(shared_page[i]) * c.page_size, to = static_cast<int64_t>(have[i]) * c.page_size;
+    const int64_t units = slot[i] * row_bytes(c) / 16, all = units * 2 * c.layers;
+    for (int64_t u = tid; u < all; u += kBlock) {
+      const int y = static_cast<int>(u / units);
+      const int64_t at = u - y * units;
+      reinterpret_cast<uint4*>(cache_row(c, y >> 1, y & 1, to))[at] =
+          __ldcg(reinterpret_cast<const uint4*>(cache_row(c, y >> 1, y & 1, from)) + at);
     }
   }
 }
@@ -207,15 +256,6 @@ __device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int
     for (int k = 0; k < 4; ++k) d[i + k * blockDim.x] = w[k];
   }
   for (; i < n; i += blockDim.x) d[i] = __ldcg(s + i);
-}
-
-__device__ __forceinline__ int64_t row_bytes(const attn_cache_t& c) {
-  return static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2);
-}
-// K (kv = 0) or V of layer l, row `row` of its pages.
-__device__ __forceinline__ uint8_t* cache_row(const attn_cache_t& c, int l, int kv, int64_t row) {
-  return static_cast<uint8_t*>(kv ? c.v : c.k) +
-         (static_cast<int64_t>(l) * c.pages * c.page_size + row) * row_bytes(c);
 }
 
 // Block (i, 0) writes the table row and references of fork i; block (i, 1 + y) copies
@@ -441,7 +481,7 @@ static cudaError_t grant_smem(const void* kern, size_t smem) {
 
 cudaError_t launch_alloc(const attn_cache_t& c, const int32_t* slots, const int32_t* want, int n, int32_t* granted,
                          int* err, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(c.slots) + 3 * n) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(c.slots) + 4 * n) * sizeof(int);
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<false>), smem);
   if (e != cudaSuccess) return e;
   return launch_after(grant_kernel<false>, 1, kBlock, smem, st, c, slots, want, n, granted, static_cast<ForkItem*>(nullptr), err);

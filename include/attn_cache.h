@@ -68,8 +68,10 @@ ATTN_API attn_status_t attn_rope(const attn_rope_plan_t* plan, int inverse, attn
  * lies in page page_table[s][p / page_size], row p % page_size, in every layer.
  * refs[page] counts the slots that hold a page; 0 means free.  A slot of lens[s]
  * tokens holds exactly ceil(lens[s] / page_size) pages; entries behind those are not
- * read.  A page that is not full is held by one slot only (attn_cache_fork copies it).
- * Tokens in a shared page are shared: fork a slot when its tokens have been appended.
+ * read.  Slots share full pages (attn_cache_fork copies one that is not full).
+ * Tokens in a shared page are shared: fork a slot when its tokens have been appended.  A slot that
+ * attn_cache_compact cuts back inside a shared page keeps it; attn_cache_alloc gives it a page of its
+ * own, the tokens copied, before it grows.
  * page_size: a power of two from 16 to 1024; d 64 or 128; slots <= 8192.
  * Page operations (alloc, free, fork, copy, compact) that share a cache must not run
  * at the same time: issue them on one stream. */
@@ -88,8 +90,9 @@ typedef struct {
 /*
  * Grows slot slots[i] to new_lens[i] >= lens tokens, i < n <= 8192.  Pages are handed out
  * in order of i, lowest page number first; request i is granted (granted[i] = 1) iff
- * it needs no page or the pages needed by requests 0..i do not exceed the free ones.  One
- * not granted changes nothing.  A slot named twice, a shorter length or one
+ * it needs no page or the pages needed by requests 0..i do not exceed the free ones.  A slot
+ * that grows inside a page which another slot holds too needs one more, in place of that page, whose
+ * tokens are copied in every layer.  One not granted changes nothing.  A slot named twice, a shorter length or one
  * beyond max_pages: not granted (the first of two counts), error recorded.
  */
 ATTN_API attn_status_t attn_cache_alloc(const attn_cache_t* cache, const int32_t* slots,
