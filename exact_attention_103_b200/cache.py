@@ -189,7 +189,7 @@ class Rope:
             def index(turns):
                 return dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
             lo = max(math.floor(index(beta_fast)), 0)
-            hi = min(math.ceil(index(beta_slow)), dim // 2 - 1)
+            hi = min(math.ceil(index(beta_slow)), dim - 1)  # may lie behind the last pair
             for i, f in enumerate(freqs):
                 ramp = min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
                 freqs[i] = f * (1 - ramp) + f / factor * ramp
