@@ -96,7 +96,7 @@ struct TreeParams {
   float scale_log2, o_scale, tau, p_shift;
   float* part;     // [grid][2][D / 4][256][4] unnormalised O: four columns of neighbouring rows
                    // lie together, as the lanes that write and join them are neighbouring rows
-  float2* stat;    // [grid][2][256] (maximum in log2 units, sum)
+  float2* stat;    // [grid][2][256] (maximum in log2 units, sum; sum -1: a page was out of range)
   int4* head;      // [grid] the item whose first tiles this CTA left unfinished
   int* err;
 };
@@ -304,7 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sb = smem_u32(smem);
   auto bar = [&](int i) -> uint32_t { return sb + Lay::BAR_OFF + 8 * i; };
   uint32_t* misc = reinterpret_cast<uint32_t*>(smem + Lay::MISC_OFF);
-  // misc[0] TMEM base, misc[1] abort flag, misc[2] items finished, misc[4..16) sums of the warps
+  // misc[0] TMEM base, misc[1] abort flag, misc[2] items finished, misc[3] items whose K copies have all
+  // been issued, misc[4..16) sums of the warps, misc[16..32) page out of range in item i (% 16)
   int* tab = reinterpret_cast<int*>(smem + Lay::TABLE_OFF);
   int *t_cum = tab, *t_cu = t_cum + p.B + 1, *t_slot = t_cu + p.B + 1, *t_len = t_slot + p.B, *t_per = t_len + p.B;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(Lay::B_KVFULL + i), 1);
       mbar_init(bar(Lay::B_KVEMPTY + i), 1);
     }
-    misc[1] = misc[2] = 0u;
+    misc[1] = misc[2] = misc[3] = 0u;
     fence_barrier_init();
   }
   if (warp == 9) {
@@ -439,10 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar(b), parity, wc, timeout_code(site)));
   };
 
-  // Until this CTA has finished its first k items.  A count, not a barrier's phase: the waiting
+  // Until misc[word] has counted this CTA's first k items.  A count, not a barrier's phase: the waiting
   // role may be several items ahead.
-  auto wait_items = [&](int k) -> bool {
-    const uint32_t at = sb + Lay::MISC_OFF + 8;
+  auto wait_count = [&](int word, int k) -> bool {
+    const uint32_t at = sb + Lay::MISC_OFF + 4 * word;
     const uint64_t t0 = global_timer_ns();
     bool good = true;
     while (true) {
@@ -459,6 +460,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return __all_sync(0xffffffffu, good);
   };
+  auto wait_items = [&](int k) -> bool { return wait_count(2, k); };
+  auto count_items = [&](int word, int k) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sb + Lay::MISC_OFF + 4 * word), "r"(k) : "memory");
+  };
+  // Pages out of range, found by the producer of K for item i: nothing of such an item is written.  That
+  // producer is at most 9 items ahead of the softmax warps' epilogue: the S of two items fit in TMEM beside the
+  // one they are at, the K ring holds four tiles more, and one waits for its slot.
+  volatile uint32_t* bad_page = misc + 16;
   // E4M3: softmax warp w writes its eighth of an item's queries, from q slot nq on: each row is
   // scaled by the power of two that brings its largest value into [128, 256), hi = E4M3(x), lo =
   // E4M3(x - hi).  A row is held by D / 8 lanes, 8 values each; a warp's rows are 8 kRows apart.
@@ -597,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       was_swapped = it.swapped;
-      ++items;
+      bool out_of_range = false;
       for (int j = it.j0; j < it.j1; ++j, ++n, pos += kBN, from += per_tile) {
         if (from == 32) {
           from = 0;
@@ -611,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool copies = lane < per_tile && mine < it.len;
         int at = p.rows;
         if (static_cast<unsigned>(page) < static_cast<unsigned>(p.pages)) at = p.layer_row + (page << p.page_shift) + (mine & in_page);
-        else if (copies) record_invalid(p.err, kSitePage);
+        else if (copies) out_of_range = true;
         const int boxes = min(per_tile, (it.len - pos + p.box_rows - 1) / p.box_rows);
         if (n >= static_cast<uint32_t>(NR)) {
           ok = wait(Lay::B_KVEMPTY + (is_k ? 0 : NR) + slot, ((n / NR) - 1) & 1u, kSiteTKvEmpty);
@@ -626,6 +635,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if (is_k) {
+        out_of_range = __any_sync(0xffffffffu, out_of_range);
+        if (lane == 0) {
+          if (out_of_range) record_invalid(p.err, kSitePage);
+          bad_page[items & 15] = out_of_range;
+          count_items(3, items + 1);
+        }
+      }
+      ++items;
     }
     // This warp's copies have landed before the CTA may exit.
     for (uint32_t i = n > static_cast<uint32_t>(NR) ? n - NR : 0u; i < n; ++i)
@@ -651,8 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int items = 0;
     auto finished = [&]() {
       ++items;
-      if (threadIdx.x == 0)
-        asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(sb + Lay::MISC_OFF + 8), "r"(items) : "memory");
+      if (threadIdx.x == 0) count_items(2, items);
     };
     uint32_t w_s_phase = 0, w_pv = 0, w_wg = 0, votes = 0;  // swapped items; w_pv: P~ handed over
     // An item of few rows, scores transposed: a thread holds one key of the tile and all
@@ -853,6 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(Lay::B_ML));
       if (!wait(Lay::B_ML, m_phase, kSiteTMerge)) return false;
       m_phase ^= 1u;
+      if (!wait_count(3, items + 1)) return false;
+      const bool bad = bad_page[items & 15] != 0;
       const bool whole = it.j0 == 0 && it.j1 == it.kvt;
       const int64_t slot = static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0);
       if (key < rows) {
@@ -873,11 +892,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         al[key] = w1 * f0;
         if (s == 0) {
           const int t2 = token_of(key, p), g2 = key - t2 * p.G;
-          if (whole)
+          if (!whole)
+            p.stat[slot * (2 * kBM) + key] = make_float2(m, bad ? -1.f : sum);
+          else if (!bad)
             p.lse[static_cast<int64_t>(it.h * p.G + g2) * p.T + it.q0 + it.tok0 + t2] =
                 sum > 0.f ? (m + __log2f(sum) - p.p_shift) * kLn2 : -INFINITY;
-          else
-            p.stat[slot * (2 * kBM) + key] = make_float2(m, sum);
         }
       }
       if (!meet()) return false;
@@ -904,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int row = c + i;
-            if (row < rows) {
+            if (row < rows && !bad) {
               if (whole)
                 p.o[(static_cast<int64_t>(it.q0 + it.tok0 + t2) * p.Hq + it.h * p.G + g2) * D + key] = __float2bfloat16(v[i]);
               else
@@ -1187,6 +1206,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       o_phase ^= 1u;
       tc_fence_after();
+      ok = wait_count(3, items + 1);
+      if (!ok) break;
+      const bool bad = bad_page[items & 15] != 0;
       const bool whole = it.j0 == 0 && it.j1 == it.kvt;
       if (busy) {
         const int g = rr - tl * p.G;
@@ -1221,7 +1243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (use_own) add(t_o + term * kLoLanes, a0);
               if (use_other) add(t_x + term * kLoLanes, a1);
             }
-            if (valid && whole) {
+            if (valid && whole && !bad) {
               uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + 32 * c + mine_at);
 #pragma unroll
               for (int i = 0; i < NV / 8; ++i)
@@ -1229,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     pack_bf16x2(v[8 * i + 2] * inv, v[8 * i + 3] * inv),
                                     pack_bf16x2(v[8 * i + 4] * inv, v[8 * i + 5] * inv),
                                     pack_bf16x2(v[8 * i + 6] * inv, v[8 * i + 7] * inv));
-            } else if (valid) {
+            } else if (valid && !bad) {
               float4* dst = part + (c * 8 + mine_at / 4) * (2 * kBM);
 #pragma unroll
               for (int i = 0; i < NV / 4; ++i)
@@ -1245,12 +1267,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           write(std::integral_constant<int, 1>{});
         }
         if (valid && (it.two || s == 0) && !(it.duo && lane >= 16)) {
-          if (whole) {
+          if (!whole)
+            p.stat[slot * (2 * kBM) + slot_row] = make_float2(m_ref, bad ? -1.f : l);
+          else if (!bad)
             p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] =
                 l > 0.f ? (m_ref + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
-          } else {
-            p.stat[slot * (2 * kBM) + slot_row] = make_float2(m_ref, l);
-          }
         }
       }
       // The next item's P~V may write either O only when both warpgroups have read them, and
@@ -1553,6 +1574,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
   const int parts = hd.w - c + 1;
   constexpr int N = 8;
   float m = -INFINITY, l = 0.f, acc[4] = {};
+  bool bad = false;
   for (int k0 = 0; k0 < parts; k0 += N) {
     float2 st[N];
     float4 v[N];
@@ -1568,7 +1590,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
     }
     float top = m;
 #pragma unroll
-    for (int k = 0; k < N; ++k) top = fmaxf(top, st[k].x);
+    for (int k = 0; k < N; ++k) {
+      top = fmaxf(top, st[k].x);
+      bad |= st[k].y < 0.f;
+    }
     if (top == -INFINITY) continue;  // no key of these parts is seen
     const float old = fast_exp2(m - top);
     m = top;
@@ -1586,6 +1611,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
       acc[3] = fmaf(w, v[k].w, acc[3]);
     }
   }
+  if (bad) return;
   const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
   const int64_t row = static_cast<int64_t>(hd.x + t) * p.Hq + hd.y * p.G + g;
   *reinterpret_cast<uint2*>(p.o + row * D + 4 * col) =

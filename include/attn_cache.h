@@ -164,6 +164,7 @@ ATTN_API attn_status_t attn_rope_append(const attn_cache_t* cache, int layer,
  * What pages hold behind a sequence's end never counts; a key that no token of its sequence
  * sees may hold anything, but values of a sequence's own tokens must be finite.  A cu_q
  * that decreases or leaves [0, T] makes the whole call do nothing (error recorded).
+ * Rows that would read a page out of range are left alone (error recorded).
  * An E4M3 cache is read as it is.  Queries keep 2^-17 of their row's largest value (the sum of two
  * E4M3 terms).  A probability keeps 2^-8 of itself, as in a bf16 cache, down to 2^-20 of its row's
  * largest one, and 2^-28 of that below (the sum of three E5M2 terms).

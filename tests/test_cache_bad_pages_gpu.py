@@ -1,0 +1,56 @@
+"""A page number out of range in a slot's table: the operators leave that sequence alone, do the
+others, and report it."""
+import pytest
+import torch
+
+import exact_attention_103_b200 as ea
+import test_tree_gpu as tree
+
+pytestmark = pytest.mark.gpu
+ints = tree.ints
+BAD = (-1, 10 ** 6, 2 ** 31 - 1, -2 ** 31)
+
+
+def reported():
+    with pytest.raises(ea.AttnError) as e:
+        ea.get_device_status()
+    assert e.value.status == ea.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dtype,d", tree.KINDS)
+@pytest.mark.parametrize("n,G", [(1, 4), (6, 4), (12, 4), (25, 4), (50, 4)])
+def test_attention(dtype, d, n, G):
+    """Any page of a sequence, in every form, in short items and in ones that many SMs share."""
+    ctx = [100, 9000, 300, 64]
+    c = tree.build(ctx, [n] * 4, 2, d, 64, dtype, seed=5)
+    mask = tree.tree_mask([n] * 4, 7)
+    q, cu, o, lse = tree.run(c, [n] * 4, 2 * G, mask)
+    keep = c.page_table.clone()
+    for i, (b, m) in enumerate([(0, 0), (0, 1), (1, 0), (1, 60), (1, (9000 + n - 1) // 64), (2, 3), (3, 0)]):
+        c.page_table[b, m] = BAD[i % 4]
+        o2, lse2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+        ea.tree_fwd(c, q, cu, mask=mask, out=o2, lse=lse2)
+        reported()
+        own = slice(b * n, (b + 1) * n)
+        assert (o2[own] == 7).all() and (lse2[:, own] == 7).all()
+        o2[own], lse2[:, own] = o[own], lse[:, own]
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        c.page_table.copy_(keep)
+    o2, lse2 = ea.tree_fwd(c, q, cu, mask=mask)
+    ea.get_device_status()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_attention_of_many_short_sequences():
+    """Items far shorter than what the copies run ahead."""
+    ctx = [3 + b % 5 for b in range(600)]
+    c = tree.build(ctx, [1] * 600, 2, 64, 16, seed=6)
+    q, cu, o, lse = tree.run(c, [1] * 600, 4)
+    bad = list(range(0, 600, 7))
+    c.page_table[bad, 0] = c.pages
+    o2, lse2 = torch.full_like(o, 7.0), torch.full_like(lse, 7.0)
+    ea.tree_fwd(c, q, cu, out=o2, lse=lse2)
+    reported()
+    assert (o2[bad] == 7).all() and (lse2[:, bad] == 7).all()
+    o2[bad], lse2[:, bad] = o[bad], lse[:, bad]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
