@@ -260,8 +260,9 @@ __device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int
 
 // Block (i, 0) writes the table row and references of fork i; block (i, 1 + y) copies
 // the tail's tokens of one layer's K or V.  A second launch, as the copies need blocks on every SM:
-// 48 forks of 8 layers (with the freeing of their slots before) 15 us, 27 MB of them copies.
-__global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* err) {
+// 48 forks of 8 layers (with the freeing of their slots before) 15 us, 27 MB of them copies.  A source with
+// a page out of range is found here, where its row is read: block (i, 0) takes the grant back.
+__global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int32_t* granted, int* err) {
   let_next_launch();
   wait_for_previous();
   const int4 w = __ldcg(reinterpret_cast<const int4*>(items + blockIdx.x));
@@ -272,10 +273,23 @@ __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* er
   const int32_t* from = c.page_table + static_cast<int64_t>(it.src) * c.max_pages;
   if (blockIdx.y == 0) {
     int32_t* to = c.page_table + static_cast<int64_t>(it.dst) * c.max_pages;
+    bool bad = false;
+    for (int m = threadIdx.x; m < full + (part ? 1 : 0); m += blockDim.x) {
+      const int p = __ldcg(from + m);
+      bad |= p < 0 || p >= c.pages;
+    }
+    if (__syncthreads_or(bad)) {
+      if (threadIdx.x == 0) {
+        record_invalid(err, kSitePage);
+        granted[blockIdx.x] = 0;
+        c.lens[it.dst] = 0;
+        if (part) c.refs[it.fresh] = 0;
+      }
+      return;
+    }
     for (int m = threadIdx.x; m < full; m += blockDim.x) {
       const int p = __ldcg(from + m);
-      if (p < 0 || p >= c.pages) record_invalid(err, kSitePage);
-      else atomicAdd(c.refs + p, 1);
+      atomicAdd(c.refs + p, 1);
       to[m] = p;
     }
     if (part && threadIdx.x == 0) to[full] = it.fresh;
@@ -283,10 +297,7 @@ __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int* er
   }
   if (!part) return;
   const int old = __ldcg(from + full);
-  if (old < 0 || old >= c.pages) {
-    if (threadIdx.x == 0) record_invalid(err, kSitePage);
-    return;
-  }
+  if (old < 0 || old >= c.pages) return;
   const int y = blockIdx.y - 1;
   copy_bytes(cache_row(c, y >> 1, y & 1, static_cast<int64_t>(old) * c.page_size),
              cache_row(c, y >> 1, y & 1, static_cast<int64_t>(it.fresh) * c.page_size), part * row_bytes(c));
@@ -499,7 +510,7 @@ cudaError_t launch_fork(const attn_cache_t& c, const int32_t* src, const int32_t
   ForkItem* items = static_cast<ForkItem*>(ws);
   e = launch_after(grant_kernel<true>, 1, kBlock, smem, st, c, src, dst, n, granted, items, err);
   if (e != cudaSuccess) return e;
-  return launch_after(fork_kernel, dim3(n, 1 + 2 * c.layers), 256, 0, st, c, items, err);
+  return launch_after(fork_kernel, dim3(n, 1 + 2 * c.layers), 256, 0, st, c, items, granted, err);
 }
 
 cudaError_t launch_copy(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int* err, cudaStream_t st) {

@@ -108,7 +108,8 @@ ATTN_API attn_status_t attn_cache_free(const attn_cache_t* cache, const int32_t*
  * Forks slot src[i] into the empty slot dst[i], i < n <= 8192: full pages are shared
  * (refs + 1), the tokens of a last page that is not full are copied, in every layer, to
  * a new page (handed out as by attn_cache_alloc).  granted as there; a destination
- * that holds tokens, equals its source or is named twice is refused, error recorded.
+ * that holds tokens, equals its source or is named twice is refused, error recorded, and so is a source
+ * with a page out of range (whose copy's page counts as needed in this call).
  * workspace: attn_cache_fork_workspace_size(n) bytes, 16-byte aligned.
  */
 ATTN_API attn_status_t attn_cache_fork(const attn_cache_t* cache, const int32_t* src,

@@ -54,3 +54,30 @@ def test_attention_of_many_short_sequences():
     assert (o2[bad] == 7).all() and (lse2[:, bad] == 7).all()
     o2[bad], lse2[:, bad] = o[bad], lse[:, bad]
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_fork():
+    c = tree.build([40, 40, 48, 0, 0, 0], [0] * 6, 2, 64, 16, layers=2, spare=4)
+    state = [t.clone() for t in (c.page_table, c.lens, c.refs)]
+    for slot, m, src, dst in ((0, 0, [0, 1, 2], [3, 4, 5]), (0, 2, [1, 0, 2], [4, 3, 5]), (2, 1, [0, 2, 1], [5, 3, 4])):
+        for page in BAD:
+            for t, s in zip((c.page_table, c.lens, c.refs), state):
+                t.copy_(s)
+            c.page_table[slot, m] = page
+            before = [t.clone() for t in (c.page_table, c.lens, c.refs)]
+            granted = c.fork(ints(src), ints(dst))
+            reported()
+            assert granted.tolist() == [int(s != slot) for s in src]
+            assert c.lens[3] == 0 and (c.page_table[3] == before[0][3]).all()
+            for s, t in zip(src, dst):
+                if s != slot:
+                    full = int(state[1][s]) // 16
+                    assert c.lens[t] == state[1][s] and torch.equal(c.page_table[t, :full], c.page_table[s, :full])
+            held = torch.zeros_like(c.refs)
+            for s in range(6):
+                for p in c.page_table[s, :-(-int(c.lens[s]) // 16)].tolist():
+                    if 0 <= p < c.pages:
+                        held[p] += 1
+            # the page that the bad number stands for keeps the count its owner gave it
+            lost = before[2] - torch.stack([held, before[2]]).amin(0)
+            assert torch.equal(c.refs, held + lost)
