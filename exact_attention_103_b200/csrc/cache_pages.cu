@@ -398,9 +398,10 @@ __device__ __forceinline__ int check_kept(const attn_cache_t& c, const int32_t* 
     const int p = row[i];  // by way of L1: read again for the moves
     if (p >= drafted || p <= (i ? row[i - 1] : -1)) {
       bad = kSitePath;
-    } else if (p != i) {  // a token moves here: no other slot may hold the page
-      const int page = __ldcg(c.page_table + static_cast<int64_t>(k.slot) * c.max_pages + (k.base + i) / c.page_size);
-      if (page < 0 || page >= c.pages || __ldcg(c.refs + page) != 1) bad = kSitePage;
+    } else if (p != i) {  // a token moves: from a page of the cache, to one that no other slot holds
+      const int32_t* table = c.page_table + static_cast<int64_t>(k.slot) * c.max_pages;
+      const int from = __ldcg(table + (k.base + p) / c.page_size), to = __ldcg(table + (k.base + i) / c.page_size);
+      if (from < 0 || from >= c.pages || to < 0 || to >= c.pages || __ldcg(c.refs + to) != 1) bad = kSitePage;
     }
   }
   for (int j = t; slots && j < b; j += n)
@@ -416,7 +417,7 @@ constexpr int kMoves = 128;  // moves whose rows are looked up together
 // moves may go before their writes.  The release is a launch of its own, as the blocks of all layers
 // read the table.  64 trees, 8 layers, with the grant before: 16 us, bound by latency.
 __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
-                               const int32_t* accepted, const int32_t* slots, int* err) {
+                               const int32_t* accepted, const int32_t* slots) {
   __shared__ int64_t from[kMoves], to[kMoves];
   let_next_launch();
   wait_for_previous();
@@ -434,11 +435,9 @@ __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const 
     __syncthreads();
     for (int i = threadIdx.x; i < m; i += blockDim.x) {
       const int x = k.base + path[static_cast<int64_t>(b) * width + m0 + i], y = k.base + m0 + i;
-      const int px = __ldcg(row + x / c.page_size), py = __ldcg(row + y / c.page_size);
-      const bool ok = px >= 0 && px < c.pages && py >= 0 && py < c.pages;
-      if (!ok) record_invalid(err, kSitePage);
-      from[i] = (ok && x != y) ? static_cast<int64_t>(px) * c.page_size + (x & (c.page_size - 1)) : -1;
-      to[i] = static_cast<int64_t>(py) * c.page_size + (y & (c.page_size - 1));
+      // the pages of tokens that move have been checked
+      from[i] = x == y ? -1 : static_cast<int64_t>(__ldcg(row + x / c.page_size)) * c.page_size + (x & (c.page_size - 1));
+      to[i] = static_cast<int64_t>(__ldcg(row + y / c.page_size)) * c.page_size + (y & (c.page_size - 1));
     }
     __syncthreads();
     if (col >= rb) continue;
@@ -531,7 +530,7 @@ cudaError_t launch_compact(const attn_cache_t& c, const int32_t* cu_q, const int
   const int64_t words = static_cast<int64_t>(c.heads) * c.d * (c.e4m3 ? 1 : 2) / 16;
   const int threads = words >= 256 ? 256 : static_cast<int>((words + 31) / 32 * 32);
   const int z = static_cast<int>((words + threads - 1) / threads);
-  const cudaError_t e = launch_after(compact_kernel, dim3(B, 2 * c.layers, z), threads, 0, st, c, cu_q, path, width, accepted, slots, err);
+  const cudaError_t e = launch_after(compact_kernel, dim3(B, 2 * c.layers, z), threads, 0, st, c, cu_q, path, width, accepted, slots);
   if (e != cudaSuccess) return e;
   int blocks = 1;  // of the cluster: a power of two
   while (blocks < kCutBlocks && blocks * kCutWarps < B) blocks *= 2;

@@ -81,3 +81,22 @@ def test_fork():
             # the page that the bad number stands for keeps the count its owner gave it
             lost = before[2] - torch.stack([held, before[2]]).amin(0)
             assert torch.equal(c.refs, held + lost)
+
+
+def test_compact():
+    """The page that a token moves from, or to."""
+    for m in (1, 3):  # tokens 16.., 48.. of 10 + 50
+        for page in BAD:
+            c = tree.build([10, 10], [50, 50], 2, 64, 16, layers=2, seed=7)
+            other = tree.build([10, 10], [50, 50], 2, 64, 16, layers=2, seed=7)
+            path = ints([[0, 3, 8, 41], [0, 3, 8, 41]])
+            c.page_table[0, m] = page
+            before = [t.clone() for t in (c.page_table, c.lens, c.refs)]
+            # token 10 + 8 (page 1) moves to 12, token 51 (page 3) to 13
+            c.compact(ints([0, 50, 100]), path, ints([4, 4]))
+            reported()
+            other.compact(ints([0, 50]), path[1:], ints([4]), slots=ints([1]))
+            for name in ("k", "v"):
+                assert torch.equal(getattr(c, name).view(torch.uint8), getattr(other, name).view(torch.uint8))
+            assert c.lens.tolist() == [60, 14] and torch.equal(c.page_table[0], before[0][0])
+            assert torch.equal(c.page_table[1], other.page_table[1])
