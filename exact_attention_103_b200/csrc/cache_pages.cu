@@ -396,7 +396,7 @@ __device__ __forceinline__ int check_kept(const attn_cache_t& c, const int32_t* 
   const int32_t* row = path + static_cast<int64_t>(b) * width;
   for (int i = t; i < k.count; i += n) {
     const int p = row[i];  // by way of L1: read again for the moves
-    if (p >= drafted || p <= (i ? row[i - 1] : -1)) {
+    if (p < i || p >= drafted || p <= (i ? row[i - 1] : -1)) {  // increasing from 0 on, so never below i
       bad = kSitePath;
     } else if (p != i) {  // a token moves: from a page of the cache, to one that no other slot holds
       const int32_t* table = c.page_table + static_cast<int64_t>(k.slot) * c.max_pages;

@@ -100,3 +100,14 @@ def test_compact():
                 assert torch.equal(getattr(c, name).view(torch.uint8), getattr(other, name).view(torch.uint8))
             assert c.lens.tolist() == [60, 14] and torch.equal(c.page_table[0], before[0][0])
             assert torch.equal(c.page_table[1], other.page_table[1])
+
+
+def test_compact_along_bad_paths():
+    """Path entries that name no token: negative behind negative, far out, falling."""
+    c = tree.build([40], [20], 2, 64, 16, layers=2, seed=8, fill=1.0)
+    before = [t.clone() for t in (c.page_table, c.lens, c.refs, c.k, c.v)]
+    low = -2 ** 31
+    for path in ([low, low + 1, low + 2], [-3, -2, -1], [-1, 0, 1], [5, 4, 6], [0, 0, 1], [0, 1, 20], [0, 1, 2 ** 31 - 1], [1, low, 3]):
+        c.compact(ints([0, 20]), ints([path]), ints([3]))
+        reported()
+        assert all(torch.equal(x, y) for x, y in zip(before, (c.page_table, c.lens, c.refs, c.k, c.v)))
