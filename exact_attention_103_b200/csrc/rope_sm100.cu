@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
 }
 
-// Append: rows of q, k, v of each token, in that order.  Rotated keys and the values go to
+// Append: rows of q, k, v of each token, in that order (none of a token that has no row in the cache).  Rotated keys and the values go to
 // the token's row of the cache.  A step of decoding has few tokens, so what counts is the
 // chain of loads behind one another: offsets, slots and the first rows come together
 // (each block takes all offsets and slots into shared memory), then lengths, then pages.
@@ -349,8 +349,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
       if (r >= r1) break;
       const Row row = row_at(r);
       const Token& tk = tok[row.ti];
-      if (!tk.live) continue;
-      if (row.which != 0 && (tk.row < 0 || again[row.ti])) continue;
+      if (tk.row < 0 || again[row.ti]) continue;  // of no sequence, or of one that cannot be appended
       const Unit& k = row.which == 2 ? plain : turned;
       float x[8], y[8];
       widen(raw[i][0], x);

@@ -145,7 +145,9 @@ ATTN_API attn_status_t attn_cache_compact(const attn_cache_t* cache, const int32
  * positions: int32[T], the rotary position (a drafted token's depth behind its context);
  * NULL: the token's place in the cache.  q, k: rows of bf16 (batch strides unused); q->dst
  * receives the rotated queries (q may be NULL); k->dst and v->dst are not used.  Rotated keys
- * and values are rounded once, to the cache's type (E4M3: divided by the scale, saturated).
+ * and values are rounded once, to the cache's type (E4M3: divided by the scale, saturated).  Of a
+ * token that has no row in the cache (error recorded) the query is left alone too; of two
+ * sequences with one slot the second is refused so.
  */
 ATTN_API attn_status_t attn_rope_append(const attn_cache_t* cache, int layer,
                                         const attn_rope_plan_t* plan, const attn_rows_t* q,

@@ -111,3 +111,31 @@ def test_compact_along_bad_paths():
         c.compact(ints([0, 20]), ints([path]), ints([3]))
         reported()
         assert all(torch.equal(x, y) for x, y in zip(before, (c.page_table, c.lens, c.refs, c.k, c.v)))
+
+
+def test_append_leaves_the_queries_too():
+    """A sequence that cannot be appended: neither its rows of the cache nor its rotated queries."""
+    c = tree.build([20, 20, 20], [4, 4, 4], 1, 64, 16, fill=2.0)
+    plan = ea.Rope(64)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v = (torch.randn((12, h, 64), generator=g, device="cuda").to(torch.bfloat16) for h in (3, 1, 1))
+    cu = ints([0, 4, 8, 12])
+    want = ea.rope_append(c, q, k, v, cu, plan=plan)
+    ea.get_device_status()
+    keep = c.page_table.clone()
+
+    def again(**kw):
+        out = torch.full_like(q, 7.0)
+        k0, v0 = c.k.clone(), c.v.clone()
+        ea.rope_append(c, q, -k, -v, cu, plan=plan, out=out, **kw)
+        reported()
+        assert (out[4:8] == 7).all() and torch.equal(out[:4], want[:4]) and torch.equal(out[8:], want[8:])
+        page = int(keep[1, 1])
+        assert torch.equal(c.k[0, page], k0[0, page]) and torch.equal(c.v[0, page], v0[0, page])
+    c.page_table[1, 1] = -1
+    again()
+    c.page_table.copy_(keep)
+    again(slots=ints([0, 9, 2]))
+    again(slots=ints([0, 0, 2]))
+    c.lens[1] = 3
+    again()
