@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_
   if (a.slots) {
     // Two sequences with one slot would write the same rows: the first one counts.
     for (int i = 0; i < ntok; ++i) {
-      if (!tok[i].live || tok[i].row < 0) continue;
+      if (!tok[i].live) continue;
       const int b = static_cast<int>(tok[i].b), slot = slots[b];
       if (i > 0 && tok[i - 1].live && tok[i - 1].b == b) continue;  // seen with its first token
       for (int j = threadIdx.x; j < b; j += kAppendThreads)

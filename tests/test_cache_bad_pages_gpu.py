@@ -139,3 +139,17 @@ def test_append_leaves_the_queries_too():
     again(slots=ints([0, 0, 2]))
     c.lens[1] = 3
     again()
+
+
+def test_append_to_one_slot_twice_behind_a_bad_page():
+    """The second of two sequences with one slot is refused whatever the pages of its first tokens are."""
+    for _ in range(20):
+        c = tree.build([10], [20], 2, 64, 16, fill=1.0)
+        g = torch.Generator(device="cuda").manual_seed(2)
+        x = torch.randn((40, 2, 64), generator=g, device="cuda").to(torch.bfloat16)
+        page = int(c.page_table[0, 1])
+        c.page_table[0, 0] = c.pages
+        ea.rope_append(c, None, x, x, ints([0, 20, 40]), slots=ints([0, 0]))
+        reported()
+        for t in (c.k, c.v):
+            assert torch.equal(t[0, page, :14], x[6:20])
