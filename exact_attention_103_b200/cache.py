@@ -82,14 +82,23 @@ _current_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 
 
-def _stream(dev: torch.device, stream: Optional[torch.cuda.Stream], *made) -> int:
-    """The raw stream of a call; tensors this call made are kept until it has run there."""
+def _stream(dev: torch.device, stream: Optional[torch.cuda.Stream]) -> int:
+    """The raw stream of a call."""
+    return _current_stream(dev.index) if stream is None else stream.cuda_stream
+
+
+def made_for(stream: Optional[torch.cuda.Stream], make, *args, **kw) -> torch.Tensor:
+    """A tensor that a call on `stream` (None: the current one) writes first.  Its memory is that
+    stream's: a block of the caller's stream may still be in use there by work queued before.  It is kept
+    for the caller's stream too, where the result is read when that stream has waited for the other."""
     if stream is None:
-        return _current_stream(dev.index)
-    for t in made:
-        if t is not None:
-            t.record_stream(stream)
-    return stream.cuda_stream
+        return make(*args, **kw)
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if caller != stream:
+        t.record_stream(caller)
+    return t
 
 
 def _on(dev: torch.device, f, *args) -> None:
@@ -221,11 +230,10 @@ def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
         k_shape = k.shape
         if len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
             raise ValueError("q and k must hold the same tokens and head dim")
-    made = ()
     if out is None:
-        q_out, k_out = made = (torch.empty_like(q, memory_format=torch.contiguous_format),
-                               None if k is None else
-                               torch.empty_like(k, memory_format=torch.contiguous_format))
+        q_out = made_for(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
+        k_out = None if k is None else made_for(stream, torch.empty_like, k,
+                                                memory_format=torch.contiguous_format)
     else:
         q_out, k_out = (out, None) if isinstance(out, torch.Tensor) else out
         _cuda(q_out, "out of q")
@@ -243,7 +251,7 @@ def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
         tokens = B * N
     pos = None if positions is None else _list(positions, "positions", dev, tokens)
     _on(dev, lib.attn_rope, plan._ref, inverse, kind, rows, 1 if k is None else 2, shape[-1], B, N,
-        cu, pos, _stream(dev, stream, *made))
+        cu, pos, _stream(dev, stream))
     return q_out if k is None else (q_out, k_out)
 
 
@@ -347,10 +355,10 @@ class KVCache:
         grows inside a page which another slot holds too (``compact`` may leave one) gets a page of its
         own in its place, its tokens copied."""
         lib, dev, n = _lib_of(), self.device, slots.numel()
-        granted = torch.empty(n, dtype=torch.int32, device=dev)
+        granted = made_for(stream, torch.empty, n, dtype=torch.int32, device=dev)
         _on(dev, lib.attn_cache_alloc, self._ref, _list(slots, "slots", dev),
             _list(new_lens, "new_lens", dev, n), n, granted.data_ptr(),
-            _stream(dev, stream, granted))
+            _stream(dev, stream))
         return granted
 
     def free(self, slots: torch.Tensor, stream: Optional[torch.cuda.Stream] = None) -> None:
@@ -365,12 +373,12 @@ class KVCache:
         tokens of a last page that is not full are copied to a new one, in every layer.
         Returns ``granted`` as ``alloc`` does."""
         lib, dev, n = _lib_of(), self.device, src.numel()
-        granted = torch.empty(n, dtype=torch.int32, device=dev)
-        ws = torch.empty(max(lib.attn_cache_fork_workspace_size(n), 16), dtype=torch.uint8,
-                         device=dev)
+        granted = made_for(stream, torch.empty, n, dtype=torch.int32, device=dev)
+        ws = made_for(stream, torch.empty, max(lib.attn_cache_fork_workspace_size(n), 16),
+                      dtype=torch.uint8, device=dev)
         _on(dev, lib.attn_cache_fork, self._ref, _list(src, "src", dev),
             _list(dst, "dst", dev, n), n, granted.data_ptr(), ws.data_ptr(), ws.numel(),
-            _stream(dev, stream, granted, ws))
+            _stream(dev, stream))
         return granted
 
     def copy(self, src: torch.Tensor, dst: torch.Tensor,
@@ -416,14 +424,14 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
     T, _, d = shape = k.shape if k.dim() == 3 else (0, 0, 0)
     if d != cache.d or v.shape != shape:
         raise ValueError(f"k and v must be [T, heads, {cache.d}]")
-    made = q_row = None
+    q_row = None
     if q is not None:
         _cuda(q, "q")
         q_shape = q.shape
         if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
             raise ValueError(f"q must be [T, Hq, {cache.d}]")
         if out is None:
-            out = made = torch.empty_like(q, memory_format=torch.contiguous_format)
+            out = made_for(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
         else:
             _cuda(out, "out")
         q_row = _row(*_rows(q, out, "q", _bf16, dev, q_shape, False))
@@ -437,7 +445,7 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
         q_row, k_row, v_row, B, T, cu,
         None if slots is None else _list(slots, "slots", dev, B),
         None if positions is None else _list(positions, "positions", dev, T),
-        _stream(dev, stream, made))
+        _stream(dev, stream))
     return None if q is None else out
 
 
@@ -466,14 +474,13 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
     T, Hq, _ = shape
     cu = _list(cu_q, "cu_q", dev)
     B = cu_q.numel() - 1
-    made_o = made_l = None
     if out is None:
-        out = made_o = torch.empty_like(q)
+        out = made_for(stream, torch.empty_like, q)
     elif not (out.is_cuda and out.device == dev and out.dtype is torch.bfloat16
               and out.shape == shape and out.is_contiguous()):
         raise ValueError("out must be like q")
     if lse is None:
-        lse = made_l = torch.empty(Hq, T, dtype=torch.float32, device=dev)
+        lse = made_for(stream, torch.empty, Hq, T, dtype=torch.float32, device=dev)
     elif not (lse.is_cuda and lse.device == dev and lse.dtype is torch.float32
               and tuple(lse.shape) == (Hq, T) and lse.is_contiguous()):
         raise ValueError("lse must be a contiguous float32 [Hq, T]")
@@ -485,9 +492,9 @@ def tree_fwd(cache: KVCache, q: torch.Tensor, cu_q: torch.Tensor,
         if mask.dim() != 2 or mask.shape[0] != T or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous [T, width]")
         m, width = mask.data_ptr(), mask.shape[1]
-    ws = torch.empty(cache._ws, dtype=torch.uint8, device=dev)
+    ws = made_for(stream, torch.empty, cache._ws, dtype=torch.uint8, device=dev)
     _on(dev, lib.attn_tree_fwd, cache._ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(),
         Hq, B, T, cu, None if slots is None else _list(slots, "slots", dev, B), m, width,
         1.0 / math.sqrt(d) if scale is None else float(scale), ws.data_ptr(), cache._ws,
-        _stream(dev, stream, ws, made_o, made_l))
+        _stream(dev, stream))
     return out, lse
