@@ -126,6 +126,7 @@ def _check(status: int):
 
 
 _cache._lib_of, _cache._check = load_library, _check
+_made_for = _cache.made_for
 
 
 def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> int:
@@ -201,13 +202,13 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
         lse_shape = (H, q.shape[0])
         opts.total_tokens = q.shape[0]
     if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        out = _made_for(stream, torch.empty, q.shape, dtype=torch.bfloat16, device=q.device)
     else:
         _need(out, "out")
         if out.shape != q.shape:
             raise ValueError("out has the wrong shape")
     if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+        lse = _made_for(stream, torch.empty, lse_shape, dtype=torch.float32, device=q.device)
     else:
         _need(lse, "lse", torch.float32)
         if tuple(lse.shape) != lse_shape:
@@ -396,9 +397,9 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse:
         _need(cu_seqlens, "cu_seqlens", torch.int32)
         B, H, N = cu_seqlens.numel() - 1, q.shape[1], int(max_seqlen)
         total, cu_ptr = q.shape[0], cu_seqlens.data_ptr()
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q)
+    dq, dk, dv = (_made_for(stream, torch.empty_like, q) for _ in range(3))
     ws_bytes = lib.attn_bwd_workspace_size(B, H, N, d, total, int(bool(deterministic)))
-    ws = torch.empty(max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
+    ws = _made_for(stream, torch.empty, max(ws_bytes, 256), dtype=torch.uint8, device=q.device)
     with torch.cuda.device(q.device):
         opts = BwdOpts(0 if window is None else 1, -1 if window is None else int(window[0]),
                        -1 if window is None else int(window[1]), 0,

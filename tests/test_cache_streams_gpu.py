@@ -80,3 +80,24 @@ def test_results_read_on_the_callers_stream():
         torch.cuda.synchronize()
         assert torch.equal(z, want) and torch.equal(w, other)
     ea.get_device_status()
+
+
+def test_forward_and_backward():
+    """The dense calls: outputs, gradients and the backward's workspace."""
+    side = torch.cuda.Stream()
+    q, k, v, do = (torch.randn(1, 2048, 8, 128, device="cuda").to(torch.bfloat16) for _ in range(4))
+    want = ea.fwd(q, k, v, causal=True)
+    grads = ea.bwd(q, k, v, *want, do, causal=True)
+    busy = torch.randn(6000, 6000, device="cuda")
+    torch.cuda.synchronize()
+    for _ in range(5):
+        (busy @ busy).sum()
+        late = [torch.zeros_like(x) for x in (*want, *grads)]  # written behind the product
+        del late
+        got = ea.fwd(q, k, v, causal=True, stream=side)
+        back = ea.bwd(q, k, v, *want, do, causal=True, stream=side)
+        over = [torch.full_like(q, 3.0) for _ in range(6)]  # what the backward released, if it could
+        torch.cuda.synchronize()
+        del over
+        assert all(torch.equal(x, y) for x, y in zip((*got, *back), (*want, *grads)))
+    ea.get_device_status()
