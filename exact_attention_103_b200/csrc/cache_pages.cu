@@ -484,9 +484,12 @@ __global__ void __launch_bounds__(kCutWarps * 32) cut_kernel(const attn_cache_t 
 
 }  // namespace
 
+// The lists of grant_kernel, one of slots and four of requests, are raised to the most that any call needs
+// (8192 of each), never to this call's own size, which another thread's smaller call would lower again
+// before the launch.
 static cudaError_t grant_smem(const void* kern, size_t smem) {
-  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem))
-                          : cudaSuccess;
+  constexpr int most = (8192 + 4 * 8192) * sizeof(int);
+  return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) : cudaSuccess;
 }
 
 cudaError_t launch_alloc(const attn_cache_t& c, const int32_t* slots, const int32_t* want, int n, int32_t* granted,
