@@ -285,6 +285,17 @@ __device__ __forceinline__ void load_scores(uint32_t at, float (&x)[N]) {
   for (int i = 0; i < N; ++i) x[i] = __uint_as_float(w[i]);
 }
 
+// Weight of a part with maximum x and sum l beside a joint maximum m.  A part that saw nothing has none;
+// one whose sum is not a number (then its maximum may be anything, as maxima pass over NaN) is kept, so
+// that the row's sum is none either.
+__device__ __forceinline__ float part_weight(float x, float l, float m) {
+  return x == -INFINITY && l == 0.f ? 0.f : fast_exp2(x - m);
+}
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }  // 0: a row that sees nothing
+__device__ __forceinline__ float natural_lse(float m, float l, float p_shift) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l) - p_shift) * kLn2;
+}
+
 // Bits [0, k) of word g of a 128-bit set of columns.
 __device__ __forceinline__ uint32_t below(int k, int g) {
   k -= 32 * g;
@@ -885,9 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2[i] = (g2[192 + key] + g2[256 + key]) + (g2[320 + key] + g2[384 + key]);
         }
         const float m = fmaxf(m2[0], m2[1]);
-        const float w0 = m2[0] == -INFINITY ? 0.f : fast_exp2(m2[0] - m), w1 = m2[1] == -INFINITY ? 0.f : fast_exp2(m2[1] - m);
+        const float w0 = part_weight(m2[0], l2[0], m), w1 = part_weight(m2[1], l2[1], m);
         const float sum = l2[0] * w0 + l2[1] * w1;
-        const float f0 = whole ? (sum > 0.f ? 1.f / sum : 0.f) * p.o_scale : 1.f;
+        const float f0 = whole ? inverse_sum(sum) * p.o_scale : 1.f;
         nm[key] = w0 * f0;
         al[key] = w1 * f0;
         if (s == 0) {
@@ -895,8 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!whole)
             p.stat[slot * (2 * kBM) + key] = make_float2(m, bad ? -1.f : sum);
           else if (!bad)
-            p.lse[static_cast<int64_t>(it.h * p.G + g2) * p.T + it.q0 + it.tok0 + t2] =
-                sum > 0.f ? (m + __log2f(sum) - p.p_shift) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(it.h * p.G + g2) * p.T + it.q0 + it.tok0 + t2] = natural_lse(m, sum, p.p_shift);
         }
       }
       if (!meet()) return false;
@@ -1197,8 +1207,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_phase ^= 1u;
         const float2 other = ml[(s ^ 1) * kBM + r];
         const float m = fmaxf(m_ref, other.x);
-        a0 = m_ref == -INFINITY ? 0.f : fast_exp2(m_ref - m);
-        a1 = other.x == -INFINITY ? 0.f : fast_exp2(other.x - m);
+        a0 = part_weight(m_ref, l, m);
+        a1 = part_weight(other.x, other.y, m);
         l = l * a0 + other.y * a1;
         m_ref = m;
       }
@@ -1216,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t slot = static_cast<int64_t>(cta) * 2 + (it.j0 == 0 ? 1 : 0);
         const int slot_row = (it.two ? s * kBM : 0) + rr;
         float4* part = reinterpret_cast<float4*>(p.part) + slot * (2 * kBM) * (D / 4) + slot_row;
-        const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
+        const float inv = inverse_sum(l) * p.o_scale;
         // Columns of this warpgroup; a stream that took no tile has nothing in its O.
         const int c_lo = it.two ? 0 : s * (D / 64), c_hi = it.two ? D / 32 : (s + 1) * (D / 64);
         const bool use_own = any, use_other = !it.two && (s != 0 || it.j1 - it.j0 > 1 || full_tile(it, 0));
@@ -1270,8 +1280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!whole)
             p.stat[slot * (2 * kBM) + slot_row] = make_float2(m_ref, bad ? -1.f : l);
           else if (!bad)
-            p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] =
-                l > 0.f ? (m_ref + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
+            p.lse[static_cast<int64_t>(it.h * p.G + g) * p.T + it.q0 + tok] = natural_lse(m_ref, l, p.p_shift);
         }
       }
       // The next item's P~V may write either O only when both warpgroups have read them, and
@@ -1594,16 +1603,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
       top = fmaxf(top, st[k].x);
       bad |= st[k].y < 0.f;
     }
-    if (top == -INFINITY) continue;  // no key of these parts is seen
-    const float old = fast_exp2(m - top);
+    const float old = m == top ? 1.f : fast_exp2(m - top);
     m = top;
     l *= old;
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] *= old;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float w = st[k].x == -INFINITY ? 0.f : fast_exp2(st[k].x - m);
-      if (w == 0.f) continue;
+      const float w = part_weight(st[k].x, st[k].y, m);
+      if (w == 0.f && st[k].y == st[k].y) continue;
       l = fmaf(w, st[k].y, l);
       acc[0] = fmaf(w, v[k].x, acc[0]);
       acc[1] = fmaf(w, v[k].y, acc[1]);
@@ -1612,12 +1620,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Tr
     }
   }
   if (bad) return;
-  const float inv = (l > 0.f ? 1.f / l : 0.f) * p.o_scale;
+  const float inv = inverse_sum(l) * p.o_scale;
   const int64_t row = static_cast<int64_t>(hd.x + t) * p.Hq + hd.y * p.G + g;
   *reinterpret_cast<uint2*>(p.o + row * D + 4 * col) =
       make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   if (col == 0)
-    p.lse[static_cast<int64_t>(hd.y * p.G + g) * p.T + hd.x + t] = l > 0.f ? (m + __log2f(l) - p.p_shift) * kLn2 : -INFINITY;
+    p.lse[static_cast<int64_t>(hd.y * p.G + g) * p.T + hd.x + t] = natural_lse(m, l, p.p_shift);
 }
 
 constexpr int kMaxSmem = 232448;

@@ -163,7 +163,7 @@ ATTN_API attn_status_t attn_rope_append(const attn_cache_t* cache, int layer,
  * the last n_b).  Among the drafted tokens, token t sees token j iff mask[t][j] != 0
  * (mask: one byte each, [T, mask_width], t counted over the batch, j within its sequence;
  * n_b <= mask_width <= 256), or j <= t when mask is NULL.  A token that sees nothing gets
- * O = 0 and LSE = -inf.  n_b = 0 is fine; rows outside [cu_q[0], cu_q[B]) are left alone.
+ * O = 0 and LSE = -inf; one that sees a score which is not a number gets NaN in both.  n_b = 0 is fine; rows outside [cu_q[0], cu_q[B]) are left alone.
  * What pages hold behind a sequence's end never counts; a key that no token of its sequence
  * sees may hold anything, but values of a sequence's own tokens must be finite.  A cu_q
  * that decreases or leaves [0, T] makes the whole call do nothing (error recorded).
