@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint8_t* m = p.mask + static_cast<int64_t>(it.q0 + it.tok0) * p.mask_width + jl;
 #pragma unroll 4
               for (int t2 = 0; t2 < it.nt; ++t2)
-                if (__ldg(m + static_cast<int64_t>(t2) * p.mask_width) != 0) {
+                if (m[static_cast<int64_t>(t2) * p.mask_width] != 0) {
                   see[0] |= below((t2 + 1) * p.G, 0) & ~below(t2 * p.G, 0);
                   see[1] |= below((t2 + 1) * p.G, 1) & ~below(t2 * p.G, 1);
                 }
@@ -1087,7 +1087,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   for (int c = 0; c < 2; ++c) {
                     const int jl = col + 32 * c;
                     w[i][c] = (t0 + i <= t_hi && jl >= 0 && jl < it.n)
-                                  ? __ldg(rows + static_cast<int64_t>(t0 + i) * p.mask_width + jl)
+                                  ? rows[static_cast<int64_t>(t0 + i) * p.mask_width + jl]
                                   : 0;
                   }
 #pragma unroll

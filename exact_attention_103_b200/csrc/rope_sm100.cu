@@ -168,7 +168,7 @@ __device__ __forceinline__ void fill_table(float* table, const Token* tok, int n
   const float sign = a.inverse ? -1.f : 1.f;
   for (int i = threadIdx.x; i < ntok * half; i += threads) {
     const int k = i / half, f = i - k * half;
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(tok[k].pos)) * __ldg(a.plan.turns + f);
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(tok[k].pos)) * a.plan.turns[f];
     const float half_turns = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
     float s, c;
     sincospif(half_turns, &s, &c);
