@@ -22,27 +22,28 @@ __device__ __forceinline__ int pages_of(int tokens, int page_size) {
 }
 
 // Exclusive prefix sum of one value per thread of the block, and the block's total.
-__device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T* warp_sums, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = v;
+  T incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    const T n = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += n;
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    int s = warp_sums[lane];
+    T s = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, s, o);
+      const T n = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += n;
     }
     warp_sums[lane] = s;
   }
   __syncthreads();
-  const int before = warp ? warp_sums[warp - 1] : 0;
+  const T before = warp ? warp_sums[warp - 1] : 0;
   total = warp_sums[31];
   __syncthreads();
   return before + incl - v;
@@ -74,11 +75,12 @@ struct alignas(16) ForkItem {
 template <bool FORK>
 __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, const int32_t* a, const int32_t* b, int n,
                                                           int32_t* granted, ForkItem* items, int* err) {
-  extern __shared__ int shared[];
-  __shared__ int warp_sums[32];
-  int* owner = shared;          // [slots]
-  int* upto = owner + c.slots;  // [n]
-  int* have = upto + n;         // [n] pages held before (-1: refused)
+  extern __shared__ int64_t shared[];
+  __shared__ int64_t need_sums[32];
+  __shared__ int page_sums[32];
+  int64_t* upto = shared;  // [n] in 64 bits: each request may ask for as many pages as a table row has entries
+  int* owner = reinterpret_cast<int*>(upto + n);  // [slots]
+  int* have = owner + c.slots;  // [n] pages held before (-1: refused)
   int* slot = have + n;         // [n] the slot that is written
   int* shared_page = slot + n;  // [n] alloc: the page whose tokens are copied (-1: none)
   const int tid = threadIdx.x;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
     if (s >= 0 && s < c.slots) atomicMin(&owner[s], i);
   }
   __syncthreads();
-  int sum = 0;
+  int64_t sum = 0;
   for (int i = i0; i < i1; ++i) {
     const int s = slot[i];
     bool ok = s >= 0 && s < c.slots && owner[s] == i;
@@ -158,8 +160,8 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
     sum += need;
     upto[i] = sum;  // within the thread; the threads before are added below
   }
-  int total;
-  const int before = block_scan(sum, warp_sums, total);
+  int64_t total;
+  const int64_t before = block_scan(sum, need_sums, total);
   for (int i = i0; i < i1; ++i) upto[i] += before;
   __syncthreads();
   // The free pages, lowest first: each thread counts its pages of a stretch, a
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
   for (int base = 0; base < c.pages && found < total; base += kBlock * kPagesPerThread) {
     const int p0 = base + tid * kPagesPerThread;
     int here;
-    int rank = found + block_scan(__popc(bits), warp_sums, here);
+    int rank = found + block_scan(__popc(bits), page_sums, here);
     unsigned next = 0;  // the next stretch loads behind this one's work
     if (found + here < total && p0 + kBlock * kPagesPerThread < c.pages) next = free_pages(p0 + kBlock * kPagesPerThread);
     int lo = 0;  // the first request with upto > rank: searched once, then followed
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
       if (FORK) {
         items[lo].fresh = page;
       } else {
-        const int k = have[lo] + rank - (lo ? upto[lo - 1] : 0);
+        const int k = have[lo] + static_cast<int>(rank - (lo ? upto[lo - 1] : 0));
         c.page_table[static_cast<int64_t>(slot[lo]) * c.max_pages + k] = page;
       }
     }
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
   __syncthreads();
   bool copies = false;
   for (int i = i0; i < i1; ++i) {
-    const int first = i ? upto[i - 1] : 0, need = upto[i] - first;
+    const int64_t first = i ? upto[i - 1] : 0, need = upto[i] - first;
     bool ok = have[i] >= 0;
     const int s = slot[i];
     if (ok && need > 0 && upto[i] > found) {
@@ -484,17 +486,17 @@ __global__ void __launch_bounds__(kCutWarps * 32) cut_kernel(const attn_cache_t 
 
 }  // namespace
 
-// The lists of grant_kernel, one of slots and four of requests, are raised to the most that any call needs
+// The lists of grant_kernel, one of slots and those of requests, are raised to the most that any call needs
 // (8192 of each), never to this call's own size, which another thread's smaller call would lower again
 // before the launch.
 static cudaError_t grant_smem(const void* kern, size_t smem) {
-  constexpr int most = (8192 + 4 * 8192) * sizeof(int);
+  constexpr int most = 8192 * (sizeof(int64_t) + 4 * sizeof(int));
   return smem > 40 * 1024 ? cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most) : cudaSuccess;
 }
 
 cudaError_t launch_alloc(const attn_cache_t& c, const int32_t* slots, const int32_t* want, int n, int32_t* granted,
                          int* err, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(c.slots) + 4 * n) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(c.slots) + 3 * n) * sizeof(int) + n * sizeof(int64_t);
   const cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<false>), smem);
   if (e != cudaSuccess) return e;
   return launch_after(grant_kernel<false>, 1, kBlock, smem, st, c, slots, want, n, granted, static_cast<ForkItem*>(nullptr), err);
@@ -506,7 +508,7 @@ cudaError_t launch_free(const attn_cache_t& c, const int32_t* slots, int n, int*
 
 cudaError_t launch_fork(const attn_cache_t& c, const int32_t* src, const int32_t* dst, int n, int32_t* granted,
                         void* ws, int* err, cudaStream_t st) {
-  const size_t smem = (static_cast<size_t>(c.slots) + 3 * n) * sizeof(int);
+  const size_t smem = (static_cast<size_t>(c.slots) + 2 * n) * sizeof(int) + n * sizeof(int64_t);
   cudaError_t e = grant_smem(reinterpret_cast<const void*>(grant_kernel<true>), smem);
   if (e != cudaSuccess) return e;
   ForkItem* items = static_cast<ForkItem*>(ws);

@@ -155,3 +155,25 @@ def test_holders_of_one_page_in_one_compaction(fill, releaser_first):
         same(keep, tokens(c, 2))
         assert c.refs[c.page_table[2, 1]] == 1 and c.refs[c.page_table[2, 0]] == 2
         sound(c)
+
+
+def test_requests_whose_sum_passes_32_bits():
+    """Each asks for almost as many pages as a row of the table has entries: none fits, none behind
+    them that needs a page, and what needs none is granted."""
+    width = (2 ** 31 - 4096) // 16
+    n = 40
+    table = torch.empty((n + 2, width), dtype=torch.int32, device="cuda")
+    table[:, :4] = -1
+    kv = torch.zeros(1, 64, 16, 1, 64, dtype=torch.bfloat16, device="cuda")
+    zero = torch.zeros(n + 2, dtype=torch.int32, device="cuda")
+    c = ea.KVCache(kv, kv.clone(), table, zero, torch.zeros(64, dtype=torch.int32, device="cuda"))
+    assert c.alloc(ints([0]), ints([20])).tolist() == [1]
+    for m in (n, 32, 17):
+        slots = list(range(1, m + 1))
+        want = [width * 16 - i % 3 for i in range(m)]
+        granted = c.alloc(ints(slots + [0, m + 1]), ints(want + [21, 5])).tolist()
+        assert granted == [0] * m + [1, 0]
+        assert c.lens.tolist()[:m + 2] == [21] + [0] * (m + 1)
+        assert c.page_table[:, :4].tolist() == [[0, 1, -1, -1]] + [[-1] * 4] * (n + 1)
+        assert c.refs.tolist() == [1, 1] + [0] * 62
+    ea.get_device_status()
