@@ -118,7 +118,8 @@ attn_status_t attn_rope(const attn_rope_plan_t* plan, int inverse, attn_type_t t
     ATTN_TRY(check_list(cu_seqlens, "cu_seqlens"));
   }
   if (positions) ATTN_TRY(check_list(positions, "positions"));
-  if (B == 0 || N == 0) return ATTN_OK;
+  // a packed batch of no sequence has no token to turn, unless positions name each token's
+  if (N == 0 || (B == 0 && !(cu_seqlens && positions))) return ATTN_OK;
   for (int i = 0; i < count; ++i)
     ATTN_TRY(check_rows(tensors[i], i ? "k" : "q", !cu_seqlens, true, type == ATTN_FP32 ? 4 : 2));
   const int64_t tokens = cu_seqlens ? N : static_cast<int64_t>(B) * N;
