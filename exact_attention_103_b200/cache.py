@@ -130,15 +130,25 @@ def _cuda(t, name: str):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _strides(t, batch: bool):
+    """The strides of batch, token and head.  That of a dimension of one element is never used, and may be
+    anything: it is left out, so that the library's check of the others' alignment holds."""
+    s = t.stride()
+    b, n, h = s[0] if batch else 0, s[-3], s[-2]
+    if (b | n | h) & 7:
+        shape = t.shape
+        b, n, h = b if batch and shape[0] > 1 else 0, n if shape[-3] > 1 else 0, h if shape[-2] > 1 else 0
+    return b, n, h
+
+
 def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
     """One entry of the library's row descriptions, checked: tensor, result (None: it has
     none), heads and the six strides of [*lead, H, d] with contiguous heads."""
     if x.dtype is not dtype or x.get_device() != dev.index:
         raise ValueError(f"{name} must be {dtype} on {dev}")
-    sx = x.stride()
-    if sx[-1] != 1 and x.numel():
+    if x.stride(-1) != 1 and x.numel():
         raise ValueError(f"the values of a head of {name} must be contiguous")
-    bx, tx, hx = sx[0] if batch else 0, sx[-3], sx[-2]
+    bx, tx, hx = _strides(x, batch)
     if y is None:
         return x.data_ptr(), 0, shape[-2], bx, tx, hx, bx, tx, hx
     if y is x:
@@ -148,10 +158,9 @@ def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
         raise ValueError(f"out of {name} must be {dtype} on {dev}")
     if y.shape != shape:
         raise ValueError(f"out of {name} has the wrong shape")
-    sy = y.stride()
-    if sy[-1] != 1 and y.numel():
+    if y.stride(-1) != 1 and y.numel():
         raise ValueError(f"the values of a head of out of {name} must be contiguous")
-    return (x.data_ptr(), y.data_ptr(), shape[-2], bx, tx, hx, sy[0] if batch else 0, sy[-3], sy[-2])
+    return (x.data_ptr(), y.data_ptr(), shape[-2], bx, tx, hx, *_strides(y, batch))
 
 
 class Rope:
