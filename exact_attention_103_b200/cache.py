@@ -101,6 +101,12 @@ def made_for(stream: Optional[torch.cuda.Stream], make, *args, **kw) -> torch.Te
     return t
 
 
+def _like(stream: Optional[torch.cuda.Stream], x: torch.Tensor) -> torch.Tensor:
+    if stream is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return made_for(stream, torch.empty_like, x, memory_format=torch.contiguous_format)
+
+
 def _on(dev: torch.device, f, *args) -> None:
     """Calls the library with `dev` current; raises on an error status."""
     if _current_device() == dev.index:
@@ -130,15 +136,10 @@ def _cuda(t, name: str):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _strides(t, batch: bool):
+def _used(shape, b: int, n: int, h: int):
     """The strides of batch, token and head.  That of a dimension of one element is never used, and may be
     anything: it is left out, so that the library's check of the others' alignment holds."""
-    s = t.stride()
-    b, n, h = s[0] if batch else 0, s[-3], s[-2]
-    if (b | n | h) & 7:
-        shape = t.shape
-        b, n, h = b if batch and shape[0] > 1 else 0, n if shape[-3] > 1 else 0, h if shape[-2] > 1 else 0
-    return b, n, h
+    return b if shape[0] > 1 else 0, n if shape[-3] > 1 else 0, h if shape[-2] > 1 else 0
 
 
 def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
@@ -146,9 +147,12 @@ def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
     none), heads and the six strides of [*lead, H, d] with contiguous heads."""
     if x.dtype is not dtype or x.get_device() != dev.index:
         raise ValueError(f"{name} must be {dtype} on {dev}")
-    if x.stride(-1) != 1 and x.numel():
+    sx = x.stride()
+    if sx[-1] != 1 and x.numel():
         raise ValueError(f"the values of a head of {name} must be contiguous")
-    bx, tx, hx = _strides(x, batch)
+    bx, tx, hx = sx[0] if batch else 0, sx[-3], sx[-2]
+    if (bx | tx | hx) & 7:
+        bx, tx, hx = _used(shape, bx, tx, hx)
     if y is None:
         return x.data_ptr(), 0, shape[-2], bx, tx, hx, bx, tx, hx
     if y is x:
@@ -158,9 +162,13 @@ def _rows(x, y, name: str, dtype, dev: torch.device, shape, batch: bool):
         raise ValueError(f"out of {name} must be {dtype} on {dev}")
     if y.shape != shape:
         raise ValueError(f"out of {name} has the wrong shape")
-    if y.stride(-1) != 1 and y.numel():
+    sy = y.stride()
+    if sy[-1] != 1 and y.numel():
         raise ValueError(f"the values of a head of out of {name} must be contiguous")
-    return (x.data_ptr(), y.data_ptr(), shape[-2], bx, tx, hx, *_strides(y, batch))
+    by, ty, hy = sy[0] if batch else 0, sy[-3], sy[-2]
+    if (by | ty | hy) & 7:
+        by, ty, hy = _used(shape, by, ty, hy)
+    return x.data_ptr(), y.data_ptr(), shape[-2], bx, tx, hx, by, ty, hy
 
 
 class Rope:
@@ -240,9 +248,8 @@ def _rope(plan: Rope, inverse: int, q, k, positions, cu_seqlens, out, stream):
         if len(k_shape) != len(shape) or k_shape[:-2] != shape[:-2] or k_shape[-1] != shape[-1]:
             raise ValueError("q and k must hold the same tokens and head dim")
     if out is None:
-        q_out = made_for(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
-        k_out = None if k is None else made_for(stream, torch.empty_like, k,
-                                                memory_format=torch.contiguous_format)
+        q_out = _like(stream, q)
+        k_out = None if k is None else _like(stream, k)
     else:
         q_out, k_out = (out, None) if isinstance(out, torch.Tensor) else out
         _cuda(q_out, "out of q")
@@ -440,7 +447,7 @@ def rope_append(cache: KVCache, q: Optional[torch.Tensor], k: torch.Tensor, v: t
         if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != d:
             raise ValueError(f"q must be [T, Hq, {cache.d}]")
         if out is None:
-            out = made_for(stream, torch.empty_like, q, memory_format=torch.contiguous_format)
+            out = _like(stream, q)
         else:
             _cuda(out, "out")
         q_row = _row(*_rows(q, out, "q", _bf16, dev, q_shape, False))
