@@ -58,6 +58,23 @@ __device__ __forceinline__ uint8_t* cache_row(const attn_cache_t& c, int l, int 
          (static_cast<int64_t>(l) * c.pages * c.page_size + row) * row_bytes(c);
 }
 
+// Copies `bytes` (a multiple of 16), 16 per thread (t of `threads`) and step, U of them in flight.
+template <int U>
+__device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int64_t bytes, int t, int threads) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int64_t n = bytes / 16;
+  int64_t i = t;
+  for (; i + (U - 1) * threads < n; i += U * threads) {
+    uint4 w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) w[k] = __ldcg(s + i + k * threads);
+#pragma unroll
+    for (int k = 0; k < U; ++k) d[i + k * threads] = w[k];
+  }
+  for (; i < n; i += threads) d[i] = __ldcg(s + i);
+}
+
 // One fork, decided by the first kernel and carried out by the second.
 struct alignas(16) ForkItem {
   int src, dst, len;  // len 0: nothing to do
@@ -67,11 +84,12 @@ struct alignas(16) ForkItem {
 // Grants requests for pages.  alloc: slot a[i] grows to b[i] tokens.  FORK: slot a[i]
 // is forked into slot b[i] (the pages of its full part and the copies follow in
 // fork_kernel).  A slot that grows inside a page which another slot holds too (compaction cut it back
-// there) gets a page of its own in its place, one page more, whose tokens this block copies itself: a launch
-// for it would cost every other call.  Shared memory: owner (first request that names a slot), upto (pages
+// there) gets a page of its own in its place, one page more, whose tokens this block copies itself, at one SM's
+// rate (44 tokens of 8 heads of 128 in 32 layers 129 us): blocks for it would cost every other call.  Shared memory: owner (first request that names a slot), upto (pages
 // needed by requests 0..i), have, slot, shared_page.  One block, bound by its round trips to memory: the requests
 // and the first 16384 reference counts, the lengths, the stores.  Measured (B200, in a graph): freeing
-// and granting 128 slots of a pool of 65536 pages 8.9 us, a grant that finds nothing to do 2.9 us.
+// and granting 128 slots of a pool of 65536 pages 9.4 us, a grant that finds nothing to do 4.2 us, one
+// that grows 64 slots inside their last pages 3.4 us (two round trips of it to look whether they are shared).
 template <bool FORK>
 __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, const int32_t* a, const int32_t* b, int n,
                                                           int32_t* granted, ForkItem* items, int* err) {
@@ -234,30 +252,10 @@ __global__ void __launch_bounds__(kBlock, 1) grant_kernel(const attn_cache_t c, 
   for (int i = 0; i < n; ++i) {
     if (shared_page[i] < 0) continue;
     const int64_t from = static_cast<int64_t>(shared_page[i]) * c.page_size, to = static_cast<int64_t>(have[i]) * c.page_size;
-    const int64_t units = slot[i] * row_bytes(c) / 16, all = units * 2 * c.layers;
-    for (int64_t u = tid; u < all; u += kBlock) {
-      const int y = static_cast<int>(u / units);
-      const int64_t at = u - y * units;
-      reinterpret_cast<uint4*>(cache_row(c, y >> 1, y & 1, to))[at] =
-          __ldcg(reinterpret_cast<const uint4*>(cache_row(c, y >> 1, y & 1, from)) + at);
-    }
+    // a warp per layer and K or V
+    for (int y = tid >> 5; y < 2 * c.layers; y += kBlock / 32)
+      copy_bytes<8>(cache_row(c, y >> 1, y & 1, from), cache_row(c, y >> 1, y & 1, to), slot[i] * row_bytes(c), tid & 31, 32);
   }
-}
-
-// Copies `bytes` (a multiple of 16) by the block, 16 bytes per thread and step.
-__device__ __forceinline__ void copy_bytes(const uint8_t* src, uint8_t* dst, int64_t bytes) {
-  const uint4* s = reinterpret_cast<const uint4*>(src);
-  uint4* d = reinterpret_cast<uint4*>(dst);
-  const int64_t n = bytes / 16;
-  int64_t i = threadIdx.x;
-  for (; i + 3 * blockDim.x < n; i += 4 * blockDim.x) {
-    uint4 w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = __ldcg(s + i + k * blockDim.x);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) d[i + k * blockDim.x] = w[k];
-  }
-  for (; i < n; i += blockDim.x) d[i] = __ldcg(s + i);
 }
 
 // Block (i, 0) writes the table row and references of fork i; block (i, 1 + y) copies
@@ -301,8 +299,8 @@ __global__ void fork_kernel(const attn_cache_t c, const ForkItem* items, int32_t
   const int old = __ldcg(from + full);
   if (old < 0 || old >= c.pages) return;
   const int y = blockIdx.y - 1;
-  copy_bytes(cache_row(c, y >> 1, y & 1, static_cast<int64_t>(old) * c.page_size),
-             cache_row(c, y >> 1, y & 1, static_cast<int64_t>(it.fresh) * c.page_size), part * row_bytes(c));
+  copy_bytes<4>(cache_row(c, y >> 1, y & 1, static_cast<int64_t>(old) * c.page_size),
+                cache_row(c, y >> 1, y & 1, static_cast<int64_t>(it.fresh) * c.page_size), part * row_bytes(c), threadIdx.x, blockDim.x);
 }
 
 __device__ __forceinline__ void drop(const attn_cache_t& c, int page, int* err) {
@@ -372,8 +370,8 @@ __global__ void copy_kernel(const attn_cache_t c, const int32_t* src, const int3
   const int64_t bytes = row_bytes(c) * c.page_size, part = bytes / chunks;
   for (int y = blockIdx.y; y < c.layers * 2 * chunks; y += gridDim.y) {
     const int lk = y / chunks, ch = y - lk * chunks;
-    copy_bytes(cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(from) * c.page_size) + ch * part,
-               cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(to) * c.page_size) + ch * part, part);
+    copy_bytes<4>(cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(from) * c.page_size) + ch * part,
+                  cache_row(c, lk >> 1, lk & 1, static_cast<int64_t>(to) * c.page_size) + ch * part, part, threadIdx.x, blockDim.x);
   }
 }
 
@@ -417,7 +415,7 @@ constexpr int kMoves = 128;  // moves whose rows are looked up together
 // bytes of the row and takes the moves in order.  Move i reads position path[i] >= i and
 // writes position i, so no later move reads what an earlier one wrote: the reads of 8
 // moves may go before their writes.  The release is a launch of its own, as the blocks of all layers
-// read the table.  64 trees, 8 layers, with the grant before: 16 us, bound by latency.
+// read the table.  64 trees, 8 layers, with the grant before: 18.4 us, bound by latency.
 __global__ void compact_kernel(const attn_cache_t c, const int32_t* cu_q, const int32_t* path, int width,
                                const int32_t* accepted, const int32_t* slots) {
   __shared__ int64_t from[kMoves], to[kMoves];
