@@ -455,12 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // role may be several items ahead.
   auto wait_count = [&](int word, int k) -> bool {
     const uint32_t at = sb + Lay::MISC_OFF + 4 * word;
-    const uint64_t t0 = global_timer_ns();
+    uint64_t t0 = 0;
     bool good = true;
     while (true) {
       uint32_t done;
       asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(done) : "r"(at) : "memory");
       if (static_cast<int>(done) >= k) break;
+      if (t0 == 0) t0 = global_timer_ns();  // not before it is needed: reading the timer is slow
       if (*wc.abort) good = false;
       if (good && global_timer_ns() - t0 > wc.limit_ns) {
         *wc.abort = 1u;
