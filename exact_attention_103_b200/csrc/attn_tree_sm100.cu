@@ -30,7 +30,7 @@
 // 2^-17 of the row's largest value.  P~ needs E4M3's precision over far more than its range, as many small
 // weights beside a large one may hold most of a row: it is rounded to fp16 and split into three E5M2
 // terms (3 bits each), off by 2^-9 of itself or 2^-28 of the row's reference.  (Two E4M3 terms lost
-// every weight below 2^-14 of the reference: with one key 11 nats above 4096 others, 40% of O.)  A term
+// every weight below 2^-14 of the reference: of a row with one key 10 nats above the others, up to 57% of O.)  A term
 // costs one more product, at twice bf16's rate; up to 64 rows the first two are rows of one product (duo
 // items) and up to 32 all of them are columns of one (swapped items).
 //
@@ -39,10 +39,11 @@
 // warps write an E4M3 cache's split queries.  Every wait is bounded; on expiry the CTA stops, drains its
 // copies and products, frees TMEM and returns.
 //
-// Measured (B200, Hq 32, 8 cache heads, d 128, us; of the copies' time at the measured bandwidth):
-// 64 ragged contexts of 512 to 8192, one token, bf16: 145 (86%).  Two contexts of 131072, 64 rows,
-// E4M3: 128 (62%; the softmax with its conversions bounds it).  A call of little work costs
-// 11 to 12: two launches and about seven round trips to memory behind one another.
+// Measured (B200, Hq 32, 8 cache heads, d 128, us of a call with cold inputs / of a replayed graph; share of the
+// copies' time at the measured bandwidth): 64 ragged contexts of 512 to 8192, one token, bf16: 145 / 145
+// (86%).  Two contexts of 131072, 64 rows, E4M3: 172 / 143 (46% / 55%; per key tile the chain S -> softmax -> P~V
+// -> next S, and 1.2 times the cache's bytes are read: rows of 128 bytes, fetched in pairs).  A call of little work:
+// 15 / 12, two launches and about seven round trips to memory behind one another.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -69,12 +70,13 @@ enum TreeSite : int {  // wait sites of the device error word (16..30)
 };
 __host__ __device__ constexpr int timeout_code(int site) { return 4 | (site << 8); }
 
-// Items of at most this many rows compute transposed scores.  Measured (8 sequences of 8192 tokens, 4
-// heads a cache head, bf16 / E4M3, us): 32 rows 65 / 58 transposed; 64 rows 80 / 81 transposed, 73 / 68
-// as one row tile, where every row has a thread and its reference stays in a register.
+// Items of at most this many rows compute transposed scores.  Measured (64 sequences of 2000 tokens, 32 rows,
+// us, transposed and not): bf16 d 128 133, 141, d 64 99, 111; E4M3 d 128 129, 143, d 64 102, 109.  64 rows (8
+// sequences of 8192 tokens, bf16 / E4M3 while that had two terms of P~): 80 / 81 transposed, 73 / 68 as one row
+// tile, where every row has a thread and its reference stays in a register.
 constexpr int kSwapped = 32;
 // E4M3 items above that and up to 64 rows: see Seg::duo.  Measured (two contexts of 131072, 64 rows,
-// us): 158 with both terms as products of their own, 138.
+// us): 188 with every term as a product of its own, 168; d 64 170, 140.
 constexpr int kDuo = 64;
 constexpr int kMinPart = 7;  // no CTA takes less of the list: the longest tile
 
@@ -139,7 +141,10 @@ struct Layout {
   // Cost of a key tile with one and with two row tiles, and of beginning an item (its mask, queries
   // and epilogue), in units of about 1000 to 1300 cycles, as homogeneous batches and then mixed ones
   // measured.  With an item at 12, 20, 28 (bf16 d 128, us): 256 single tokens over 50 to 2000 167, 157,
-  // 161; 16 trees of 48 tokens 118, 113, 113; 128 single tokens over 100 to 4000 112, 115, 120.
+  // 161; 16 trees of 48 tokens 118, 113, 113; 128 single tokens over 100 to 4000 112, 115, 120.  At 8, 10, 12
+  // (bf16 d 64): 158, 152, 150; 154, 152, 149; 111, 110, 103; 64 single tokens over 512 to 8192 96, 97, 100.  At
+  // 16, 20, 24 (E4M3, d 128 / d 64): 184, 186, 184 / 158, 160, 158; 201, 195, 192 / 162, 166, 168; 120, 125, 123 / 104,
+  // 104, 102; 64 single tokens 104, 104, 106 / 83, 84, 84.
   static constexpr int COST_ONE = !F8 && D == 128 ? 4 : 2, COST_PAIR = !F8 && D == 128 ? 7 : 4,
                        COST_ITEM = F8 || D == 128 ? 20 : 10;
   static constexpr int P_TERMS = F8 ? 3 : 1;  // products that P~V is the sum of

@@ -10,9 +10,9 @@
 //
 // Bound by HBM: every value is read once and written once.  A block takes a few whole
 // tokens, so that one table of their sines (in shared memory) serves all their heads, and
-// moves 16 values of one head per thread and step with 16-byte accesses.  Measured (B200): 2 x 8192
-// tokens, 16 + 16 heads, d 128, bf16: 46.8 us, 88% of the copy rate; a packed batch of 16 sequences
-// of 512 to 16384 tokens, half of each head rotated: 198 us, 94%.
+// moves 16 values of one head per thread and step with 16-byte accesses.  Measured (B200, a call with cold inputs /
+// a replayed graph): 2 x 8192 tokens, 16 + 16 heads, d 128, bf16: 48.3 / 46.8 us, 85% / 88% of the copy rate; a
+// packed batch of 16 sequences of 512 to 16384 tokens, half of each head rotated: 210 / 198 us, 89% / 94%.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // chain of loads behind one another: offsets, slots and the first rows come together
 // (each block takes all offsets and slots into shared memory), then lengths, then pages.
 // The rows of all tokens are dealt evenly to one wave of blocks.  Measured: 48 single tokens of 32 +
-// 8 + 8 heads 3.8 us; 32 trees of 61 tokens into an E4M3 cache 11 us (31 MB: 4.8 at the copy
+// 8 + 8 heads 3.9 us; 32 trees of 61 tokens into an E4M3 cache 11.4 us (31 MB: 4.8 at the copy
 // rate, the rest is that chain).
 template <bool F8>
 __global__ void __launch_bounds__(kAppendThreads, 4) append_kernel(const __grid_constant__ RopeArgs a, int per_block) {

@@ -100,7 +100,8 @@ ATTN_API attn_status_t attn_cache_alloc(const attn_cache_t* cache, const int32_t
                                         attn_stream_t stream);
 
 /* Empties the slots: their pages lose a reference, their table entries become -1, lens 0.
- * A slot that is empty, or named again, is a no-op. */
+ * A slot that is empty, or named again, is a no-op.  Here, and where attn_cache_compact releases pages, a page
+ * number out of range is taken from the table like the others, error recorded. */
 ATTN_API attn_status_t attn_cache_free(const attn_cache_t* cache, const int32_t* slots, int n,
                                        attn_stream_t stream);
 
@@ -171,8 +172,10 @@ ATTN_API attn_status_t attn_rope_append(const attn_cache_t* cache, int layer,
  * An E4M3 cache is read as it is.  Queries keep 2^-17 of their row's largest value (the sum of two
  * E4M3 terms).  A probability keeps 2^-8 of itself, as in a bf16 cache, down to 2^-20 of its row's
  * largest one, and 2^-28 of that below (the sum of three E5M2 terms).
- * workspace: attn_tree_workspace_size(...) bytes, 256-byte aligned; calls that run at the
- * same time need one each.  Results do not depend on timing: the same call is bitwise
+ * Unsupported: (B + T Hq / heads / 256) heads items of (max_pages page_size / 128) key tiles each that might
+ * come to more than about 3e8 tiles.
+ * workspace: attn_tree_workspace_size(d) bytes (42 MB for d 128, 21 for 64, whatever the call), 256-byte
+ * aligned; calls that run at the same time need one each.  Results do not depend on timing: the same call is bitwise
  * repeatable.
  */
 ATTN_API attn_status_t attn_tree_fwd(const attn_cache_t* cache, int layer, const void* q, void* o,
